@@ -46,9 +46,21 @@ def make_geom(heads, head_dim, frame_h, frame_w, tile_h, tile_w, scale, dtype) -
     return Geom(heads, head_dim, frame_h, frame_w, tile_h, tile_w, float(scale), dt)
 
 
+class ReqGeom(ctypes.Structure):
+    """Geometry of the requests' attention over a 4-bit cache (pbsa_req_geom)."""
+    _fields_ = [("q_heads", ctypes.c_int), ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("scale", ctypes.c_float), ("dtype", ctypes.c_int)]
+
+
+def make_req_geom(q_heads, kv_heads, head_dim, scale, dtype) -> ReqGeom:
+    dt = dtype if isinstance(dtype, int) else (PBSA_BF16 if dtype in ("bf16", torch.bfloat16) else PBSA_F32)
+    return ReqGeom(q_heads, kv_heads, head_dim, float(scale), dt)
+
+
 _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_longlong
 _SIGS = {
     "pbsa_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(Geom), _I, _I]),
     "pbsa_blockify": (_I, [ctypes.POINTER(Geom), _P, _I, _P, _I, _P, _P, _I, _P, _P]),
@@ -75,6 +87,13 @@ _SIGS = {
     "pbsa_get_device_error": (_I, [_P, _P]),
     "pbsa_selftest_wait_timeout": (_I, [_P, ctypes.c_uint, _P]),
     "pbsa_status_string": (ctypes.c_char_p, [_I]),
+    "pbsa_q4_block_bytes": (ctypes.c_size_t, [ctypes.POINTER(ReqGeom)]),
+    "pbsa_attend_q4_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(ReqGeom)]),
+    "pbsa_request_tables": (_I, [_P, _P, _I, _P, _I, _P, _P, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "pbsa_append_q4": (_I, [ctypes.POINTER(ReqGeom), _P, _L, _P, _L, _I, _P, _P, _I, _P, _P]),
+    "pbsa_expand_q4": (_I, [ctypes.POINTER(ReqGeom), _P, _I, _P, _I, _P, _P, _P, _P]),
+    "pbsa_attend_q4": (_I, [ctypes.POINTER(ReqGeom), _P, _L, _I, _P, _P, _P, _I, _I, _P, _I, _P, _I, _I, _P, _L, _P,
+                            _P, _P]),
     "pbsa_bwd_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(Geom), _I, _I, _I]),
     "pbsa_attend_bwd": (_I, [ctypes.POINTER(Geom), _P, _I, _P, _P, _I, _P, _P, _I, _P, _P, _P,
                              _P, _P, _P, _P, _P]),
@@ -283,6 +302,131 @@ def pbsa_attend_bwd(g: Geom, q, q_frames, k_pool, v_pool, pool_slots, kv_slot, k
         pool_slots, _ptr(kv_slot, torch.int32, "kv_slot"), _ptr(kv_cnt, torch.int32, "kv_cnt"), kv_ld,
         _ptr(o, dt, "o"), _ptr(d_o, dt, "d_o"), _ptr(lse, torch.float32, "lse"), _ptr(dq, dt, "dq"),
         _ptr(dk_pool, dt, "dk_pool"), _ptr(dv_pool, dt, "dv_pool"), _ptr(ws, None, "ws"), _stream(stream)))
+
+
+# ------------------------------------------------------------------ requests over a 4-bit cache
+PBSA_CAUSAL = 1
+
+
+def _dev(t, dtype, name, numel=None, index=None):
+    """Device pointer (an int) of a contiguous tensor of the call's device: `index` is the first tensor's."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.get_device() != index:
+        raise ValueError(f"{name} must be a tensor of the current CUDA device")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if numel is not None and t.numel() != numel:
+        raise ValueError(f"{name} must have {numel} elements, got {t.numel()}")
+    return t.data_ptr()
+
+
+def _tokens(t, dtype, name, heads, d, index):
+    """(pointer, elements between tokens, tokens) of [tokens, heads, d] whose tokens may lie apart."""
+    if not t.is_cuda or t.get_device() != index:
+        raise ValueError(f"{name} must be a tensor of the current CUDA device")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
+        raise ValueError(f"{name} must be [tokens, {heads}, {d}], got {list(t.shape)}")
+    n = t.shape[0]
+    if n and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), (t.stride(0) if n > 1 else heads * d), n
+
+
+def _ws(ws, index, need=256):
+    if ws is None:
+        return None
+    if not ws.is_cuda or ws.get_device() != index:
+        raise ValueError("ws must be a tensor of the current CUDA device")
+    if not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
+        raise ValueError(f"ws must be contiguous and hold {need} bytes")
+    return ws.data_ptr()
+
+
+def _st(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def pbsa_q4_block_bytes(g: ReqGeom) -> int:
+    return int(load().pbsa_q4_block_bytes(ctypes.byref(g)))
+
+
+def pbsa_attend_q4_workspace_bytes(g: ReqGeom) -> int:
+    return int(load().pbsa_attend_q4_workspace_bytes(ctypes.byref(g)))
+
+
+def _q4_pool(g, pool, pool_slots, index):
+    return _dev(pool, torch.uint8, "pool", g.kv_heads * pool_slots * pbsa_q4_block_bytes(g), index)
+
+
+def _rows(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be two-dimensional")
+    return t.shape
+
+
+def pbsa_request_tables(step_len, seq_len, block_table, free_slot, free_cnt, q_start, q_len, kv_len, free_cnt_out,
+                        slot_map, position=None, ws=None, stream=None):
+    """Sizes are the tensors': requests of ``step_len``, table_ld of ``block_table`` [requests, table_ld], slots
+    of ``free_slot``, tokens of ``slot_map``."""
+    i32, dev = torch.int32, torch.cuda.current_device()
+    R, ld = _rows(block_table, "block_table")
+    T, S = slot_map.numel(), free_slot.numel()
+    _check("pbsa_request_tables", load().pbsa_request_tables(
+        _dev(step_len, i32, "step_len", R, dev), _dev(seq_len, i32, "seq_len", R, dev), R,
+        _dev(block_table, i32, "block_table", None, dev), ld, _dev(free_slot, i32, "free_slot", None, dev),
+        _dev(free_cnt, i32, "free_cnt", 1, dev), S, T, _dev(q_start, i32, "q_start", R + 1, dev),
+        _dev(q_len, i32, "q_len", R, dev), _dev(kv_len, i32, "kv_len", R, dev),
+        _dev(free_cnt_out, i32, "free_cnt_out", 1, dev), _dev(slot_map, i32, "slot_map", None, dev) if T else None,
+        _dev(position, i32, "position", T, dev), _ws(ws, dev), _st(stream)))
+
+
+def pbsa_append_q4(g: ReqGeom, k, v, slot_map, pool, pool_slots, ws=None, stream=None):
+    """``k``, ``v`` [tokens, kv_heads, head_dim]; tokens may lie apart (a slice of a projection's output)."""
+    dt, dev = _tok_dtype(g), torch.cuda.current_device()
+    kp, kl, n = _tokens(k, dt, "k", g.kv_heads, g.head_dim, dev)
+    vp, vl, m = _tokens(v, dt, "v", g.kv_heads, g.head_dim, dev)
+    if m != n:
+        raise ValueError("k and v must have the same number of tokens")
+    _check("pbsa_append_q4", load().pbsa_append_q4(
+        g, kp, kl, vp, vl, n, _dev(slot_map, torch.int32, "slot_map", n, dev), _q4_pool(g, pool, pool_slots, dev),
+        pool_slots, _ws(ws, dev), _st(stream)))
+
+
+def pbsa_expand_q4(g: ReqGeom, pool, pool_slots, src_slot, k_pool, v_pool, ws=None, stream=None):
+    """``k_pool``, ``v_pool`` [kv_heads, len(src_slot), 64, head_dim]."""
+    dt, dev = _tok_dtype(g), torch.cuda.current_device()
+    n = src_slot.numel()
+    size = g.kv_heads * n * 64 * g.head_dim
+    _check("pbsa_expand_q4", load().pbsa_expand_q4(
+        g, _q4_pool(g, pool, pool_slots, dev), pool_slots, _dev(src_slot, torch.int32, "src_slot", None, dev), n,
+        _dev(k_pool, dt, "k_pool", size, dev), _dev(v_pool, dt, "v_pool", size, dev), _ws(ws, dev), _st(stream)))
+
+
+def pbsa_attend_q4(g: ReqGeom, q, q_start, q_len, kv_len, max_q_len, pool, pool_slots, block_table, causal, o,
+                   lse=None, ws=None, stream=None):
+    """``q``, ``o`` [tokens, q_heads, head_dim]; tokens may lie apart.  ``q_start`` holds one entry per request or
+    one more (as pbsa_request_tables writes it)."""
+    dt, i32, dev = _tok_dtype(g), torch.int32, torch.cuda.current_device()
+    qp, ql, n = _tokens(q, dt, "q", g.q_heads, g.head_dim, dev)
+    op, ol, m = _tokens(o, dt, "o", g.q_heads, g.head_dim, dev)
+    if m != n:
+        raise ValueError("o must have q's tokens")
+    R, ld = _rows(block_table, "block_table")
+    if q_start.numel() not in (R, R + 1):
+        raise ValueError(f"q_start must have {R} or {R + 1} elements, got {q_start.numel()}")
+    if ws is None:
+        raise ValueError("pbsa_attend_q4 needs a workspace")
+    _check("pbsa_attend_q4", load().pbsa_attend_q4(
+        g, qp, ql, n, _dev(q_start, i32, "q_start", None, dev), _dev(q_len, i32, "q_len", R, dev),
+        _dev(kv_len, i32, "kv_len", R, dev), R, max_q_len, _q4_pool(g, pool, pool_slots, dev), pool_slots,
+        _dev(block_table, i32, "block_table", None, dev), ld, PBSA_CAUSAL if causal else 0, op, ol,
+        _dev(lse, torch.float32, "lse", g.q_heads * n, dev),
+        _ws(ws, dev, pbsa_attend_q4_workspace_bytes(g)), _st(stream)))
 
 
 def pbsa_selftest_wait_timeout(ws, limit_us: int, stream=None):

@@ -6,6 +6,7 @@
 #include <mutex>
 #include <vector>
 
+#include "attend_q4.cuh"
 #include "common.cuh"
 #include "internal.h"
 
@@ -50,6 +51,27 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // Pool rows (H * slots * 64) must be addressable with 32-bit TMA coordinates.
 bool pool_ok(const Geo& g, int pool_slots) {
   return pool_slots > 0 && (int64_t)g.H * pool_slots * BT < ((int64_t)1 << 31);
+}
+
+pbsa_status check_req(const pbsa_req_geom* g) {
+  if (g == nullptr) return PBSA_ERR_INVALID_ARG;
+  if (g->q_heads <= 0 || g->kv_heads <= 0 || g->head_dim <= 0 || g->q_heads % g->kv_heads != 0)
+    return PBSA_ERR_INVALID_ARG;
+  if (!(g->scale > 0.f) || !isfinite(g->scale)) return PBSA_ERR_INVALID_ARG;
+  if (g->dtype != PBSA_F32 && g->dtype != PBSA_BF16) return PBSA_ERR_INVALID_ARG;
+  if (g->head_dim != 64 && g->head_dim != 128) return PBSA_ERR_UNSUPPORTED;
+  if (g->q_heads > 4096) return PBSA_ERR_UNSUPPORTED;
+  return PBSA_OK;
+}
+
+// Slots of a 4-bit pool: slot * 64 + row and head * slots + slot fit an int.
+bool q4_pool_ok(const pbsa_req_geom* g, int pool_slots) {
+  return pool_slots > 0 && (int64_t)g->kv_heads * pool_slots * BT < ((int64_t)1 << 31);
+}
+
+// Distance between tokens: at least a token, and rows 16-byte aligned.
+bool ld_ok(long long ld, long long token, int dtype) {
+  return ld >= token && ld % (dtype == PBSA_BF16 ? 8 : 4) == 0 && ld < ((long long)1 << 31);
 }
 
 // The bounded-wait path every kernel relies on, on its own: one thread waits on an mbarrier
@@ -340,6 +362,100 @@ pbsa_status pbsa_attend_bwd(const pbsa_geom* gin, const void* q, int q_frames, c
   if (nq > 512 || (int64_t)q_frames * g.tpf * g.H > ((int64_t)1 << 31)) return PBSA_ERR_UNSUPPORTED;
   return from_cuda(launch_attend_bwd(g, q, q_frames, k_pool, v_pool, pool_slots, kv_slot, kv_cnt, kv_ld,
                                      o, d_o, lse, dq, dk_pool, dv_pool, ws, static_cast<cudaStream_t>(stream)));
+}
+
+size_t pbsa_q4_block_bytes(const pbsa_req_geom* g) { return check_req(g) == PBSA_OK ? q4_block_bytes(g->head_dim) : 0; }
+
+size_t pbsa_attend_q4_workspace_bytes(const pbsa_req_geom* g) {
+  return check_req(g) == PBSA_OK ? attend_q4_ws_bytes(g->head_dim) : 0;
+}
+
+pbsa_status pbsa_request_tables(const int* step_len, const int* seq_len, int n_requests, int* block_table,
+                                int table_ld, int* free_slot, const int* free_cnt, int pool_slots, int n_tokens,
+                                int* q_start, int* q_len, int* kv_len, int* free_cnt_out, int* slot_map,
+                                int* position, void* ws, void* stream) {
+  if (step_len == nullptr || seq_len == nullptr || block_table == nullptr || free_slot == nullptr ||
+      free_cnt == nullptr || q_start == nullptr || q_len == nullptr || kv_len == nullptr || free_cnt_out == nullptr)
+    return PBSA_ERR_INVALID_ARG;
+  if (n_requests <= 0 || table_ld <= 0 || pool_slots <= 0 || n_tokens < 0) return PBSA_ERR_INVALID_ARG;
+  if (n_tokens > 0 && slot_map == nullptr) return PBSA_ERR_INVALID_ARG;
+  if ((int64_t)pool_slots * BT >= ((int64_t)1 << 31) || (int64_t)table_ld * BT >= ((int64_t)1 << 31))
+    return PBSA_ERR_INVALID_ARG;
+  if (n_requests > 8192 || n_tokens > (1 << 28)) return PBSA_ERR_UNSUPPORTED;
+  return from_cuda(launch_request_tables(step_len, seq_len, n_requests, block_table, table_ld, free_slot, free_cnt,
+                                         pool_slots, n_tokens, q_start, q_len, kv_len, free_cnt_out, slot_map,
+                                         position, ws, static_cast<cudaStream_t>(stream)));
+}
+
+pbsa_status pbsa_append_q4(const pbsa_req_geom* g, const void* k, long long k_ld, const void* v, long long v_ld,
+                           int n_tokens, const int* slot_map, void* pool, int pool_slots, void* ws, void* stream) {
+  const pbsa_status s = check_req(g);
+  if (s != PBSA_OK) return s;
+  if (n_tokens < 0 || pool == nullptr || !aligned16(pool) || !q4_pool_ok(g, pool_slots)) return PBSA_ERR_INVALID_ARG;
+  if (n_tokens == 0) return PBSA_OK;
+  if (k == nullptr || v == nullptr || slot_map == nullptr || !aligned16(k) || !aligned16(v)) return PBSA_ERR_INVALID_ARG;
+  const long long token = (long long)g->kv_heads * g->head_dim;
+  if (!ld_ok(k_ld, token, g->dtype) || !ld_ok(v_ld, token, g->dtype)) return PBSA_ERR_INVALID_ARG;
+  return from_cuda(launch_append_q4(g->kv_heads, g->head_dim, g->dtype, k, k_ld, v, v_ld, n_tokens, slot_map, pool,
+                                    pool_slots, ws, static_cast<cudaStream_t>(stream)));
+}
+
+pbsa_status pbsa_expand_q4(const pbsa_req_geom* g, const void* pool, int pool_slots, const int* src_slot, int n_slots,
+                           void* k_pool, void* v_pool, void* ws, void* stream) {
+  const pbsa_status s = check_req(g);
+  if (s != PBSA_OK) return s;
+  if (n_slots < 0 || pool == nullptr || !aligned16(pool) || !q4_pool_ok(g, pool_slots)) return PBSA_ERR_INVALID_ARG;
+  if (n_slots == 0) return PBSA_OK;
+  if (src_slot == nullptr || k_pool == nullptr || v_pool == nullptr || !aligned16(k_pool) || !aligned16(v_pool))
+    return PBSA_ERR_INVALID_ARG;
+  if (!q4_pool_ok(g, n_slots)) return PBSA_ERR_INVALID_ARG;
+  return from_cuda(launch_expand_q4(g->kv_heads, g->head_dim, g->dtype, pool, pool_slots, src_slot, n_slots, k_pool,
+                                    v_pool, ws, static_cast<cudaStream_t>(stream)));
+}
+
+pbsa_status pbsa_attend_q4(const pbsa_req_geom* g, const void* q, long long q_ld, int n_tokens, const int* q_start,
+                           const int* q_len, const int* kv_len, int n_requests, int max_q_len, const void* pool,
+                           int pool_slots, const int* block_table, int table_ld, int flags, void* o, long long o_ld,
+                           float* lse, void* ws, void* stream) {
+  const pbsa_status s = check_req(g);
+  if (s != PBSA_OK) return s;
+  if (q_start == nullptr || q_len == nullptr || kv_len == nullptr || pool == nullptr || block_table == nullptr ||
+      ws == nullptr)
+    return PBSA_ERR_INVALID_ARG;
+  if (n_tokens < 0 || n_requests <= 0 || max_q_len < 0 || table_ld <= 0 || !q4_pool_ok(g, pool_slots))
+    return PBSA_ERR_INVALID_ARG;
+  if ((flags & ~PBSA_CAUSAL) != 0 || !aligned16(pool) || !aligned16(ws)) return PBSA_ERR_INVALID_ARG;
+  if ((int64_t)table_ld * BT >= ((int64_t)1 << 31)) return PBSA_ERR_INVALID_ARG;
+  if (n_tokens == 0 || max_q_len == 0) return PBSA_OK;
+  if (q == nullptr || o == nullptr || !aligned16(q) || !aligned16(o)) return PBSA_ERR_INVALID_ARG;
+  const long long token = (long long)g->q_heads * g->head_dim;
+  if (!ld_ok(q_ld, token, g->dtype) || !ld_ok(o_ld, token, g->dtype)) return PBSA_ERR_INVALID_ARG;
+  const int group = g->q_heads / g->kv_heads;
+  if (max_q_len > n_tokens) max_q_len = n_tokens;
+  if (n_requests > 8192 || (int64_t)max_q_len * group >= ((int64_t)1 << 30)) return PBSA_ERR_UNSUPPORTED;
+  AttendQ4Params p = {};
+  p.q = q;
+  p.q_ld = q_ld;
+  p.q_start = q_start;
+  p.q_len = q_len;
+  p.kv_len = kv_len;
+  p.R = n_requests;
+  p.T = n_tokens;
+  p.max_q = max_q_len;
+  p.pool = static_cast<const uint8_t*>(pool);
+  p.pool_slots = pool_slots;
+  p.table = block_table;
+  p.table_ld = table_ld;
+  p.kv_heads = g->kv_heads;
+  p.group = group;
+  p.causal = (flags & PBSA_CAUSAL) != 0;
+  p.scale_log2 = g->scale * 1.4426950408889634f;
+  p.o = o;
+  p.o_ld = o_ld;
+  p.lse = lse;
+  p.f32 = g->dtype == PBSA_F32;
+  p.ws = ws;
+  return from_cuda(launch_attend_q4(p, g->head_dim, g->dtype, max_q_len * group, static_cast<cudaStream_t>(stream)));
 }
 
 pbsa_status pbsa_selftest_wait_timeout(void* ws, unsigned int limit_us, void* stream) {

@@ -24,7 +24,8 @@ struct Geo {
 // Kernel ids recorded with device errors.
 enum KernelId { K_BLOCKIFY = 1, K_SCORE = 2, K_ATTEND_F32 = 3, K_ATTEND_TC = 4, K_MU_SCORE = 5,
                 K_MU_SELECT = 6, K_MU_COPY = 7, K_BWD_PREP = 8, K_BWD_KV = 9, K_BWD_Q = 10,
-                K_SELFTEST = 11 };
+                K_SELFTEST = 11, K_REQ_TABLES = 12, K_Q4_APPEND = 13, K_Q4_EXPAND = 14,
+                K_Q4_ATTEND = 15 };
 
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // bound of every in-kernel wait
 
@@ -93,6 +94,21 @@ cudaError_t launch_attend_bwd(const Geo& g, const void* q, int q_frames, const v
                               const int* kv_cnt, int kv_ld, const void* o, const void* d_o,
                               const float* lse, void* dq, void* dk_pool, void* dv_pool, void* ws,
                               cudaStream_t st);
+
+// Requests over the 4-bit paged cache (d = 64 or 128; dtype is that of the token tensors).
+cudaError_t launch_request_tables(const int* step_len, const int* seq_len, int R, int* table, int ld,
+                                  int* free_slot, const int* free_cnt, int pool_slots, int T, int* q_start,
+                                  int* q_len, int* kv_len, int* free_cnt_out, int* slot_map, int* position,
+                                  void* ws, cudaStream_t st);
+cudaError_t launch_append_q4(int H, int d, int dtype, const void* k, long long k_ld, const void* v, long long v_ld,
+                             int T, const int* slot_map, void* pool, int pool_slots, void* ws, cudaStream_t st);
+cudaError_t launch_expand_q4(int H, int d, int dtype, const void* pool, int pool_slots, const int* src_slot, int n,
+                             void* k_out, void* v_out, void* ws, cudaStream_t st);
+struct AttendQ4Params;
+size_t q4_block_bytes(int d);
+size_t attend_q4_ws_bytes(int d);
+// max_rows: the most rows (tokens * query heads of a kv head) that a request of this call may have
+cudaError_t launch_attend_q4(const AttendQ4Params& p, int d, int dtype, int max_rows, cudaStream_t st);
 
 // cuTensorMapEncodeTiled, fetched from the driver at first use (no -lcuda link needed).
 void* tensor_map_encoder();

@@ -328,6 +328,101 @@ PBSA_API pbsa_status pbsa_memory_update_noalloc(const pbsa_geom* g, const float*
                                                 const int* cand_gid, int ncand, float gamma,
                                                 int* p_list, int* p_cnt, void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Requests over a 4-bit paged cache: an autoregressive model's decode, prompt and checking steps
+ * for many requests at once, over one layer's pool of 64-token blocks (the paper has no
+ * counterpart; block size, slots, lists and error reporting are those of the pools above).
+ *
+ * The 4-bit pool of a layer is [kv_heads][pool_slots][pbsa_q4_block_bytes()], 16-byte aligned.  A
+ * slot holds K and V of 64 tokens.  For each token and head, K and V each hold, over its channels x,
+ *   m = the largest bf16 <= min x,  s = the smallest bf16 >= (max x - m) / 15 (0 if max x = m, else
+ *   >= 2^-126),  c_i = round((x_i - m) / s) in 0 .. 15 (ties to even),  and stand for  s*c_i + m
+ * ((max x - m) / 15 and (x_i - m) / s are fp32 products with the fp32 1/15 and 1/s).  A token whose K
+ * or V of a head holds a value that is not finite, or a range above fp32's or bf16's, has NaN as that
+ * head's K and zero as its V: queries that attend it yield NaN, others are not touched by it.
+ * The fields' order inside a slot is the library's own: pbsa_expand_q4 reads it back.
+ *
+ * A step of the requests: pbsa_request_tables once, then per layer pbsa_append_q4 of the step's K
+ * and V and pbsa_attend_q4 of its Q.  Nothing needs the lengths on the host, so a captured step
+ * follows them.  Requests of the same table share nothing else: one slot belongs to one request. */
+
+/* Geometry: query head h reads kv head h / (q_heads / kv_heads).  head_dim 64 or 128; q_heads a
+ * multiple of kv_heads, at most 4096; dtype: the token tensors' (PBSA_BF16 or PBSA_F32). */
+typedef struct {
+  int q_heads;
+  int kv_heads;
+  int head_dim;
+  float scale;    /* softmax scale, normally 1/sqrt(d) */
+  int dtype;
+} pbsa_req_geom;
+
+/* Bytes of one slot of one head in a 4-bit pool (8704 for d = 128, 4608 for d = 64; 0: bad geometry). */
+PBSA_API size_t pbsa_q4_block_bytes(const pbsa_req_geom* g);
+/* Device workspace of pbsa_attend_q4 (error word included), whatever the lengths; zero-filled once
+ * before first use.  The calls keep nothing in it but the error word, so calls of any geometry with the
+ * same head_dim may share it in turn; calls that overlap in time (two streams, two graphs) need one each. */
+PBSA_API size_t pbsa_attend_q4_workspace_bytes(const pbsa_req_geom* g);
+
+/* Block tables and slot maps of a step.  With n_r = max(step_len[r], 0), blocks(x) = ceil(x / 64):
+ *   q_start[r] = n_0 + .. + n_{r-1} (at most n_tokens): request r's rows in the step's token tensors;
+ *   a request with step_len[r] < 0 has ended: its blocks are given back and kv_len[r] = 0;
+ *   request r is served iff its rows end within n_tokens, blocks(seq_len[r] + n_r) <= table_ld, and
+ *   it needs no new block or the blocks asked for by the requests up to r (those that pass the first
+ *   two conditions) are at most the free ones and those given back in this call;
+ *   served:      q_len[r] = n_r, kv_len[r] = seq_len[r] + n_r, its new blocks enter block_table;
+ *   not served:  q_len[r] = 0, kv_len[r] = seq_len[r], its rows have slot_map = -1.
+ * The free stack free_slot[0 .. free_cnt) hands out from its top; blocks given back are pushed first,
+ * in request order.  slot_map[t] = slot * 64 + row of row t's token, position[t] = its place in its
+ * request; -1 for rows that belong to no served request (rows behind the last request among them).
+ *  step_len, seq_len  [n_requests] (n_requests <= 8192).
+ *  block_table  in/out [n_requests][table_ld]: row r lists request r's slots; other entries are kept.
+ *  free_slot    in/out [pool_slots];  free_cnt [1].
+ *  q_start out [n_requests + 1];  q_len, kv_len out [n_requests];  free_cnt_out out [1];
+ *  slot_map out [n_tokens];  position nullable out [n_tokens].
+ *  kv_len may be seq_len, and free_cnt_out may be free_cnt (a state kept in place); otherwise outputs
+ *  and inputs are distinct.  With both kept apart, the same call can be repeated.
+ * A length outside [0, 64 table_ld], a free count outside [0, pool_slots] or a slot outside the pool is
+ * recorded (ws, nullable) and the request or row is not served; a bad length counts as 0. */
+PBSA_API pbsa_status pbsa_request_tables(const int* step_len, const int* seq_len, int n_requests, int* block_table,
+                                int table_ld, int* free_slot, const int* free_cnt, int pool_slots, int n_tokens,
+                                int* q_start, int* q_len, int* kv_len, int* free_cnt_out, int* slot_map,
+                                int* position, void* ws, void* stream);
+
+/* K and V of the step's tokens into the 4-bit pool.
+ *  k, v   [n_tokens][kv_heads][d], token t at k + t * k_ld elements (k_ld >= kv_heads * d; rows 16-byte
+ *         aligned), e.g. slices of one projection's output.
+ *  slot_map [n_tokens]: slot * 64 + row; -1 skips the token (its k and v are not read); any other value
+ *         outside the pool is skipped and recorded.  Entries >= 0 are distinct; what a row named twice
+ *         holds is undefined. */
+PBSA_API pbsa_status pbsa_append_q4(const pbsa_req_geom* g, const void* k, long long k_ld, const void* v,
+                           long long v_ld, int n_tokens, const int* slot_map, void* pool, int pool_slots, void* ws,
+                           void* stream);
+
+/* Slots of the 4-bit pool as dense blocks: s*c + m, rounded to the geometry's dtype, of all 64 tokens of
+ * slot src_slot[i] into block i of k_pool and v_pool [kv_heads][n_slots][64][d] -- pools as pbsa_attend
+ * reads.  src_slot[i] = -1 leaves block i as it is; another id outside the pool does too and is recorded. */
+PBSA_API pbsa_status pbsa_expand_q4(const pbsa_req_geom* g, const void* pool, int pool_slots, const int* src_slot,
+                           int n_slots, void* k_pool, void* v_pool, void* ws, void* stream);
+
+/* Attention of the requests' queries over the 4-bit cache.  For token i of request r and query head h
+ *   o = sum_j softmax_j(scale * q . k_j) v_j,  lse = ln sum_j exp(scale * q . k_j)
+ * over the first kv_len[r] tokens of its table row; with PBSA_CAUSAL over the first
+ * kv_len[r] - q_len[r] + i + 1 (the step's tokens are the cache's last).  k_j, v_j are the values that the
+ * pool holds.  A token without keys gives o = 0 and lse = -inf.
+ *  q      [n_tokens][q_heads][d] with q_ld elements between tokens; request r's rows are q_start[r] ..
+ *         q_start[r] + q_len[r] - 1.  Rows of no request are neither read nor written.
+ *  q_start, q_len, kv_len [n_requests] (n_requests <= 8192), on the device; max_q_len: no q_len is larger.
+ *  block_table [n_requests][table_ld];  o like q, with o_ld;  lse nullable out [q_heads][n_tokens].
+ *  flags  0 or PBSA_CAUSAL.
+ * A request whose numbers lie out of range (q_len > max_q_len, rows outside q, kv_len > 64 table_ld) is
+ * left out and recorded; a slot outside the pool is recorded and its tokens are left out of the sums.
+ * Deterministic for a given device. */
+#define PBSA_CAUSAL 1
+PBSA_API pbsa_status pbsa_attend_q4(const pbsa_req_geom* g, const void* q, long long q_ld, int n_tokens,
+                           const int* q_start, const int* q_len, const int* kv_len, int n_requests, int max_q_len,
+                           const void* pool, int pool_slots, const int* block_table, int table_ld, int flags, void* o,
+                           long long o_ld, float* lse, void* ws, void* stream);
+
 /* Self-test of the bounded waits (the paper has no counterpart).  Every kernel that waits on an
  * mbarrier gives up after a time limit, records PBSA_ERR_TIMEOUT in the workspace's error word
  * and returns instead of hanging.  This launches one thread that waits, with that same code, on
