@@ -39,6 +39,7 @@ namespace {
 constexpr int AQ_WARPS = 4;                       // computing warps
 constexpr int AQ_THREADS = (AQ_WARPS + 1) * 32;   // + the producer
 constexpr int AQ_STAGES = 6;
+constexpr int AQ_MIN_STEPS = 2;                   // blocks that are worth a CTA of their own
 
 template <int D, int NT>
 struct AqSmem {
@@ -100,7 +101,7 @@ __global__ void __launch_bounds__(AQ_THREADS) attend_q4_kernel(const AttendQ4Par
     fence_barrier_init();
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const Q4Share share = q4_share<AQ_THREADS>(p, ROWS, &start_s);   // has block barriers
+  const Q4Share share = q4_share<AQ_THREADS>(p, ROWS, AQ_MIN_STEPS, &start_s);   // has block barriers
   Q4Walk walk(p, share, ROWS);
 
   if (warp == AQ_WARPS) {
@@ -411,35 +412,6 @@ __global__ void __launch_bounds__(AQ_THREADS) attend_q4_kernel(const AttendQ4Par
   if (tid == 0) p.desc[blockIdx.x] = walk.desc;
 }
 
-// Joins the pieces of the tile that starts in CTA blockIdx.x and ends in a later one.
-template <int D>
-__global__ void __launch_bounds__(256) attend_q4_join_kernel(const AttendQ4Params p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Q4Desc d = p.desc[blockIdx.x];
-  if (d.pieces == 0) return;
-  constexpr int CH = D / 4, RPP = 256 / CH;
-  const int ch = threadIdx.x % CH;
-  auto at = [&](int k) { return (size_t)(k == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + k)) * p.part_rows; };
-  for (int r = threadIdx.x / CH + RPP * blockIdx.y; r < d.rows; r += RPP * gridDim.y) {
-    float M = -INFINITY;
-#pragma unroll 8
-    for (int k = 0; k < d.pieces; ++k) M = fmaxf(M, p.part_ml[at(k) + r].x);
-    float L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-    for (int k = 0; k < d.pieces; ++k) {
-      const float2 ml = p.part_ml[at(k) + r];
-      const float4 v = *reinterpret_cast<const float4*>(p.part_o + (at(k) + r) * D + 4 * ch);
-      const float f = q4_weight(ml.x, M);
-      L = fmaf(f, ml.y, L);
-      acc[0] = fmaf(f, v.x, acc[0]);
-      acc[1] = fmaf(f, v.y, acc[1]);
-      acc[2] = fmaf(f, v.z, acc[2]);
-      acc[3] = fmaf(f, v.w, acc[3]);
-    }
-    q4_write_row<D>(p, d.q0, d.row0 + r, d.h, 4 * ch, acc, M, L, ch == 0);
-  }
-}
-
 template <int D, int NT, int SPLIT>
 cudaError_t launch_t(AttendQ4Params p, cudaStream_t st) {
   auto kern = attend_q4_kernel<D, NT, SPLIT>;
@@ -454,30 +426,30 @@ cudaError_t launch_t(AttendQ4Params p, cudaStream_t st) {
   const int grid = sms * per_sm < Q4_MAX_CTAS ? sms * per_sm : Q4_MAX_CTAS;
   kern<<<grid, AQ_THREADS, smem, st>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(256);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attend_q4_join_kernel<D>, p);
+  return launch_q4_join<D>(p, grid, 1, st);
 }
 
 template <int D>
-cudaError_t launch_d(const AttendQ4Params& p, int dtype, int max_rows, cudaStream_t st) {
-  if (dtype == PBSA_F32) return launch_t<D, 1, 3>(p, st);
-  if (max_rows <= 8) return launch_t<D, 1, 1>(p, st);
-  return launch_t<D, 2, 1>(p, st);
+cudaError_t launch_d(AttendQ4Params p, int dtype, int max_rows, cudaStream_t st) {
+  p.rows_above = 0;
+  if (dtype == PBSA_F32) {
+    p.rows_to = max_rows;
+    return launch_t<D, 1, 3>(p, st);
+  }
+  // Requests of more than Q4_TC_ROWS rows fill enough of a 128-row tensor-core tile (attend_q4_tc.cu).
+  p.rows_to = max_rows < Q4_TC_ROWS ? max_rows : Q4_TC_ROWS;
+  cudaError_t e = max_rows <= 8 ? launch_t<D, 1, 1>(p, st) : launch_t<D, 2, 1>(p, st);
+  if (e != cudaSuccess || max_rows <= Q4_TC_ROWS) return e;
+  p.rows_above = Q4_TC_ROWS;
+  p.rows_to = max_rows;
+  return launch_attend_q4_tc(p, D, st);
 }
 
 }  // namespace
 
 size_t attend_q4_ws_bytes(int d) {
-  // descriptors, then the pieces' sums and rows: two pieces of at most 16 rows a CTA
-  return (size_t)WS_HEADER_BYTES + Q4_MAX_CTAS * sizeof(Q4Desc) + (size_t)2 * Q4_MAX_CTAS * 16 * (8 + 4 * (size_t)d);
+  // descriptors, then the sums and the rows of two pieces a CTA
+  return (size_t)WS_HEADER_BYTES + Q4_MAX_CTAS * sizeof(Q4Desc) + (size_t)Q4_PART_ROWS * (8 + 4 * (size_t)d);
 }
 
 cudaError_t launch_attend_q4(const AttendQ4Params& in, int d, int dtype, int max_rows, cudaStream_t st) {
@@ -486,7 +458,7 @@ cudaError_t launch_attend_q4(const AttendQ4Params& in, int d, int dtype, int max
   p.desc = reinterpret_cast<Q4Desc*>(w);
   w += Q4_MAX_CTAS * sizeof(Q4Desc);
   p.part_ml = reinterpret_cast<float2*>(w);
-  w += (size_t)2 * Q4_MAX_CTAS * 16 * sizeof(float2);
+  w += (size_t)Q4_PART_ROWS * sizeof(float2);
   p.part_o = reinterpret_cast<float*>(w);
   return d == 128 ? launch_d<128>(p, dtype, max_rows, st) : launch_d<64>(p, dtype, max_rows, st);
 }

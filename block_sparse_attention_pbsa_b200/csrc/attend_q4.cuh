@@ -8,8 +8,10 @@
 
 namespace pbsa {
 
-constexpr int Q4_MAX_CTAS = 640;   // of a grid (the workspace holds two pieces for each)
-constexpr int Q4_MIN_STEPS = 2;    // blocks that are worth a CTA of their own
+constexpr int Q4_MAX_CTAS = 640;      // of a grid of the few-rows kernel (16 rows a piece)
+constexpr int Q4_TC_MAX_CTAS = 160;   // of a grid of the tensor-core kernel (128 rows a piece)
+constexpr int Q4_PART_ROWS = 2 * (Q4_MAX_CTAS * 16 > Q4_TC_MAX_CTAS * 128 ? Q4_MAX_CTAS * 16 : Q4_TC_MAX_CTAS * 128);
+constexpr int Q4_TC_ROWS = 32;        // requests with more rows go to the tensor-core kernel
 
 // A tile that starts in this CTA and ends in a later one (pieces = 0: none).
 struct __align__(8) Q4Desc {
@@ -32,6 +34,7 @@ struct AttendQ4Params {
   long long o_ld;
   float* lse;
   int f32;
+  int rows_above, rows_to;   // this kernel's requests have rows_above < q_len * group <= rows_to
   int part_rows;             // rows of a piece in the workspace
   Q4Desc* desc;
   float2* part_ml;           // (reference maximum in log2 units, sum) of a piece's row
@@ -39,10 +42,41 @@ struct AttendQ4Params {
   void* ws;
 };
 
-// The work of one request: `tiles` row tiles a head of `blocks` blocks each.
+// sum over i in [0, n) of floor((a i + b) / m), for a, b >= 0, m > 0
+__device__ __forceinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
+  long long sum = 0;
+  while (true) {
+    sum += (n - 1) * n / 2 * (a / m) + n * (b / m);
+    a %= m;
+    b %= m;
+    const long long y = a * n + b;
+    if (y < m) return sum;
+    n = y / m;
+    b = y % m;
+    const long long t = m;
+    m = a;
+    a = t;
+  }
+}
+
+// The work of one request: row tiles of each kv head, and what a tile is charged in blocks.  Without the
+// causal rule, and for a single tile, that is what it reads.  With it, tile k (from 1) of `tile_rows`
+// rows sees past + ceil(tile_rows k / group) tokens, so it reads at most
+//   charge(k) = blocks(past) + ceil(tile_rows k / (64 group))
+// blocks; the charge has a sum in closed form and is at most a block or two above.
 struct Q4Request {
   int q0, q_len, kv_len, tiles, blocks;
-  __device__ long long steps(int heads) const { return (long long)heads * tiles * blocks; }
+  int base;          // blocks(past), or -1: every tile is charged `blocks`
+  int num, den;      // tile_rows, 64 * group
+
+  __device__ long long charged_to(int n) const {   // the first n tiles
+    if (base < 0) return (long long)n * blocks;
+    return n == 0 ? 0 : (long long)n * base + floor_sum(n, den, num, num + den - 1);
+  }
+  __device__ int charge(int mt) const {
+    return base < 0 ? blocks : base + (int)(((long long)num * (mt + 1) + den - 1) / den);
+  }
+  __device__ long long head_steps() const { return charged_to(tiles); }
 };
 
 // A request whose numbers are out of range is left out (and recorded once, by the CTA that asks).
@@ -52,14 +86,20 @@ __device__ __forceinline__ Q4Request q4_request(const AttendQ4Params& p, int r, 
   x.q_len = p.q_len[r];
   x.kv_len = p.kv_len[r];
   x.tiles = x.blocks = 0;
+  x.base = -1;
+  x.num = tile_rows;
+  x.den = BT * p.group;
   if (x.q_len == 0) return x;
   if (x.q_len < 0 || x.q_len > p.max_q || x.q0 < 0 || x.q_len > p.T - x.q0 || x.kv_len < 0 ||
       x.kv_len > (long long)p.table_ld * BT) {
     if (record) record_error(p.ws, PBSA_ERR_DEVICE_INDEX, r, K_Q4_ATTEND);
     return x;
   }
-  x.tiles = (int)(((long long)x.q_len * p.group + tile_rows - 1) / tile_rows);
+  const int rows = x.q_len * p.group;
+  if (rows <= p.rows_above || rows > p.rows_to) return x;   // the other kernel's
+  x.tiles = (rows + tile_rows - 1) / tile_rows;
   x.blocks = max(1, (x.kv_len + BT - 1) / BT);   // a request without keys has its rows written too
+  if (p.causal && x.tiles > 1) x.base = (max(x.kv_len - x.q_len, 0) + BT - 1) / BT;
   return x;
 }
 
@@ -75,13 +115,13 @@ struct Q4Share {
 
 // This CTA's share [x0, x1) of the line, and the request it starts in.  Every thread calls it.
 template <int THREADS>
-__device__ __forceinline__ Q4Share q4_share(const AttendQ4Params& p, int tile_rows, Q4Start* start) {
+__device__ __forceinline__ Q4Share q4_share(const AttendQ4Params& p, int tile_rows, int min_steps, Q4Start* start) {
   __shared__ long long sums[THREADS / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.R + THREADS - 1) / THREADS;
   const int r0 = min(tid * per, p.R), r1 = min(r0 + per, p.R);
   long long mine = 0;
-  for (int r = r0; r < r1; ++r) mine += q4_request(p, r, tile_rows, blockIdx.x == 0).steps(p.kv_heads);
+  for (int r = r0; r < r1; ++r) mine += p.kv_heads * q4_request(p, r, tile_rows, blockIdx.x == 0).head_steps();
   long long upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -98,7 +138,7 @@ __device__ __forceinline__ Q4Share q4_share(const AttendQ4Params& p, int tile_ro
     if (w == warp) before = s.total;
     s.total += sums[w];
   }
-  const long long want = (s.total + Q4_MIN_STEPS - 1) / Q4_MIN_STEPS;
+  const long long want = (s.total + min_steps - 1) / min_steps;
   s.ctas = (int)(want < gridDim.x ? want : gridDim.x);
   s.x0 = s.x1 = 0;
   if ((int)blockIdx.x < s.ctas) {
@@ -107,7 +147,7 @@ __device__ __forceinline__ Q4Share q4_share(const AttendQ4Params& p, int tile_ro
     long long at = before + upto - mine;
     if (s.x0 >= at && s.x0 < at + mine) {
       for (int r = r0; r < r1; ++r) {
-        const long long n = q4_request(p, r, tile_rows, false).steps(p.kv_heads);
+        const long long n = p.kv_heads * q4_request(p, r, tile_rows, false).head_steps();
         if (s.x0 < at + n) {
           start->r = r;
           start->off = s.x0 - at;
@@ -126,49 +166,69 @@ __device__ __forceinline__ Q4Share q4_share(const AttendQ4Params& p, int tile_ro
 // The pieces of a share, in order.  Every warp of the CTA walks them by itself.
 struct Q4Walk {
   const AttendQ4Params& p;
-  long long x, x1, total, off;
+  long long x, x1, total;
   int ctas, tile_rows;
   Q4Request req;
   int r;
+  int at;         // blocks of the current tile that lie before the next piece
   // the current piece: blocks [b0, b1) of row tile mt of head h of request r
   int h, mt, b0, b1, q0, q_len, kv_len, rows;
   int piece;      // its place in the workspace; -1: the whole tile
   Q4Desc desc;    // the tile that goes on in a later CTA
 
   __device__ Q4Walk(const AttendQ4Params& prm, const Q4Share& s, int tr)
-      : p(prm), x(s.x0), x1(s.x1), total(s.total), off(s.off), ctas(s.ctas), tile_rows(tr), r(s.r) {
+      : p(prm), x(s.x0), x1(s.x1), total(s.total), ctas(s.ctas), tile_rows(tr), r(s.r) {
     desc.pieces = 0;
-    if (x < x1) req = q4_request(p, r, tile_rows, false);
+    if (x >= x1) return;
+    // the head and row tile of the share's first step
+    req = q4_request(p, r, tile_rows, false);
+    const long long head = req.head_steps();
+    h = (int)(s.off / head);
+    const long long off = s.off - h * head;
+    int lo = 0, hi = req.tiles - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (req.charged_to(mid) <= off) lo = mid;
+      else hi = mid - 1;
+    }
+    mt = lo;
+    at = (int)(off - req.charged_to(mt));
+    charge = req.charge(mt);
   }
 
   __device__ bool next() {
     if (x >= x1) return false;
-    while (off >= req.steps(p.kv_heads)) {
-      off = 0;
-      req = q4_request(p, ++r, tile_rows, false);
+    if (at == charge) {
+      at = 0;
+      if (++mt == req.tiles) {
+        mt = 0;
+        if (++h == p.kv_heads) {
+          h = 0;
+          do req = q4_request(p, ++r, tile_rows, false);
+          while (req.tiles == 0);   // there is one: x < x1
+        }
+      }
+      charge = req.charge(mt);
     }
-    const int tile = (int)(off / req.blocks), at = (int)(off - (long long)tile * req.blocks);
-    h = tile / req.tiles;
-    mt = tile - h * req.tiles;
     q0 = req.q0;
     q_len = req.q_len;
     kv_len = req.kv_len;
-    rows = (int)min((long long)q_len * p.group, (long long)0x7fffffff);
-    const int n = (int)min((long long)(req.blocks - at), x1 - x);
-    // blocks that the tile's last row sees; the blocks behind them cost their share nothing
-    const int last = (int)min((long long)(mt + 1) * tile_rows, (long long)rows) - 1;
+    rows = q_len * p.group;
+    const int n = (int)min((long long)(charge - at), x1 - x);
+    // blocks that the tile's last row sees; what is charged above them costs its share nothing
+    const int last = min((mt + 1) * tile_rows, rows) - 1;
     const int seen = p.causal ? max(min(kv_len - q_len + last / p.group + 1, kv_len), 0) : kv_len;
     const int end = (seen + BT - 1) / BT;
     b0 = at;
     b1 = max(at, min(at + n, end));
-    if (n == req.blocks) {
+    if (n == charge) {
       piece = -1;
     } else if (at > 0) {
       piece = 2 * blockIdx.x;
     } else {
       piece = 2 * blockIdx.x + 1;
       // the CTA that holds the tile's last step: the largest i with total * i / ctas <= that step
-      const long long end_step = x + req.blocks;
+      const long long end_step = x + charge;
       const int c1 = (int)((end_step * ctas + total - 1) / total) - 1;
       desc.pieces = c1 - (int)blockIdx.x + 1;
       desc.row0 = mt * tile_rows;
@@ -177,9 +237,12 @@ struct Q4Walk {
       desc.h = h;
     }
     x += n;
-    off += n;
+    at += n;
     return true;
   }
+
+ private:
+  int charge;     // of the current tile
 };
 
 // 2^(m - M) of a piece's sums; the sums of a piece that saw no key are zeros (or NaN, which stay)
@@ -202,5 +265,52 @@ __device__ __forceinline__ void q4_write_row(const AttendQ4Params& p, int q0, in
   if (with_lse && p.lse != nullptr)
     p.lse[(size_t)head * p.T + q0 + tok] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
 }
+
+// Joins the pieces of the tile that starts in CTA blockIdx.x and ends in a later one.
+template <int D>
+__global__ void __launch_bounds__(256) attend_q4_join_kernel(const AttendQ4Params p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Q4Desc d = p.desc[blockIdx.x];
+  if (d.pieces == 0) return;
+  constexpr int CH = D / 4, RPP = 256 / CH;
+  const int ch = threadIdx.x % CH;
+  auto at = [&](int k) { return (size_t)(k == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + k)) * p.part_rows; };
+  for (int r = threadIdx.x / CH + RPP * blockIdx.y; r < d.rows; r += RPP * gridDim.y) {
+    float M = -INFINITY;
+#pragma unroll 8
+    for (int k = 0; k < d.pieces; ++k) M = fmaxf(M, p.part_ml[at(k) + r].x);
+    float L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int k = 0; k < d.pieces; ++k) {
+      const float2 ml = p.part_ml[at(k) + r];
+      const float4 v = *reinterpret_cast<const float4*>(p.part_o + (at(k) + r) * D + 4 * ch);
+      const float f = q4_weight(ml.x, M);
+      L = fmaf(f, ml.y, L);
+      acc[0] = fmaf(f, v.x, acc[0]);
+      acc[1] = fmaf(f, v.y, acc[1]);
+      acc[2] = fmaf(f, v.z, acc[2]);
+      acc[3] = fmaf(f, v.w, acc[3]);
+    }
+    q4_write_row<D>(p, d.q0, d.row0 + r, d.h, 4 * ch, acc, M, L, ch == 0);
+  }
+}
+
+// The join as a programmatic dependent of the attention kernel just launched: `grid` CTAs of that kernel,
+// `split` CTAs for the rows of each tile.
+template <int D>
+cudaError_t launch_q4_join(const AttendQ4Params& p, int grid, int split, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, split);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attend_q4_join_kernel<D>, p);
+}
+
+cudaError_t launch_attend_q4_tc(AttendQ4Params p, int d, cudaStream_t st);
 
 }  // namespace pbsa

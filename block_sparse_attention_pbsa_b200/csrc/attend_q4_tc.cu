@@ -1,0 +1,536 @@
+// Attention of the requests' queries over the 4-bit cache: the form for many query rows (bf16), on the
+// 5th-generation tensor cores.
+//
+// The mathematics is attend_q4.cu's.  128 rows (row = token * group + head of the group, so the heads that
+// share a kv head share its keys) fill one M = 128 tile, and every cached byte is used 128 times per tile:
+// the products and the exponentials bound it, and unpacking the codes must hide behind them.
+//  * Work: the line of attend_q4.cuh, with tiles of 128 rows; one CTA per SM, pieces one after another.
+//    With the causal rule a tile is charged what it sees, so long prompts are spread evenly.
+//  * Each step covers two blocks (128 keys).  Warp 0 brings the slots' bytes into a ring with bulk copies;
+//    a warpgroup of 4 warps unpacks them into shared-memory operand tiles (128-byte swizzle): K as
+//    the codes themselves (plus 128, exact in bf16), V as bf16 values s*c + m, rounded once, the bits that
+//    pbsa_expand_q4 gives.  The scores then get their scale and minimum in fp32, per key:
+//      x = s (q . (c + 128)) + (m - 128 s) sum(q),
+//    so they carry no rounding of K; rounding K to bf16 would put 2^-8 |q . k| / sqrt(d) of noise into each.
+//  * TMEM: three S/P buffers and one O accumulator (512 columns), two softmax warpgroups on alternate
+//    steps, two MMA-issuing threads, P over S as bf16, O rescaled only when the reference maximum grows
+//    by more than 2^8.  S(i+3) is issued behind PV(i), so a warpgroup never waits for its own PV.
+//    (pbsa_attend is paced the same way.)
+//  * All barriers are used once per step with a step count that runs on over the pieces (a piece without
+//    blocks takes part in none).  The ring of key scales has four places: the unpackers reach step n only when
+//    PV(n-3), and so the softmax of step n-3, is done.
+//  * Keys that a row does not see get x = -inf by a select after the scale is applied, and V of tokens
+//    that are not cached is zero, so whatever bytes lie there reach no row.
+// Waits are bounded; on expiry the error is recorded and every role runs through its pieces without
+// waiting, drains its copies and MMAs, frees TMEM and returns.
+#include <math.h>
+
+#include "attend_q4.cuh"
+
+namespace pbsa {
+namespace {
+
+constexpr int TQ_THREADS = 512;      // warpgroups: control, unpack, softmax x 2
+constexpr int TQ_MIN_STEPS = 8;      // blocks that are worth a CTA of their own
+constexpr int CST = 3, KST = 2, VST = 2, NSB = 3, SCS = 4;
+constexpr uint32_t REG_CTRL = 48, REG_UNPACK = 80, REG_SOFT = 192;   // launched with 128: 48 + 80 + 2*192 = 4*128
+static_assert(REG_CTRL + REG_UNPACK + 2 * REG_SOFT <= 4 * 128, "register split exceeds the launch");
+
+enum { T_QFULL = 0, T_CFULL = 1, T_CEMPTY = T_CFULL + CST, T_KFULL = T_CEMPTY + CST, T_KEMPTY = T_KFULL + KST,
+       T_VFULL = T_KEMPTY + KST, T_VEMPTY = T_VFULL + VST, T_SCFULL = T_VEMPTY + VST, T_SFULL = T_SCFULL + SCS,
+       T_PFULL = T_SFULL + NSB, T_PVDONE = T_PFULL + NSB, T_MMADONE = T_PVDONE + 2, T_XDONE = T_MMADONE + 1,
+       T_BARS = T_XDONE + 2 };
+
+template <int D>
+struct TqSmem {
+  static constexpr uint32_t PANELS = D / 64;
+  static constexpr uint32_t TILE = PANELS * 16384;                  // 128 rows of 64 columns a panel
+  static constexpr uint32_t STEP = 2 * Q4<D>::BYTES;
+  static constexpr uint32_t Q = 0;
+  static constexpr uint32_t K = TILE;
+  static constexpr uint32_t V = K + KST * TILE;
+  static constexpr uint32_t CODES = V + VST * TILE;
+  static constexpr uint32_t SC = CODES + CST * STEP;                // float [SCS][2][128]: per key, scale and offset
+  static constexpr uint32_t QS = SC + SCS * 1024;                   // float [128]: sums of the rows of Q
+  static constexpr uint32_t MREF = QS + 512;                        // float [2][128]
+  static constexpr uint32_t STAT = MREF + 1024;                     // float2 [2][128]
+  static constexpr uint32_t BARS = STAT + 2048;
+  static constexpr uint32_t META = BARS + T_BARS * 8;               // int [CST][2], int [SCS], TMEM address, abort flag
+  static constexpr uint32_t TOTAL = META + 4 * (2 * CST + SCS + 2);
+  static constexpr uint32_t BYTES = TOTAL + 1024;
+};
+static_assert(TqSmem<128>::BYTES <= 232448, "shared memory");
+
+__device__ __forceinline__ void fma2(float x0, float x1, float y0, float y1, float z0, float z1, float& d0, float& d1) {
+  asm("{\n\t.reg .b64 x, y, z, d;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, x, y, z;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d0), "=f"(d1) : "f"(x0), "f"(x1), "f"(y0), "f"(y1), "f"(z0), "f"(z1));
+}
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+
+template <int D>
+__global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const AttendQ4Params p) {
+  using Q = Q4<D>;
+  using SM = TqSmem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + SM::BARS);
+  volatile int* meta = reinterpret_cast<volatile int*>(sm + SM::META);          // [CST][2]: the block is there
+  volatile int* sc_ok = meta + 2 * CST;                                         // [SCS]: the same, two bits
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + SM::META) + 2 * CST + SCS;
+  volatile int* abort_flag = meta + 2 * CST + SCS + 1;
+  __shared__ Q4Start start_s;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int i = 0; i < T_BARS; ++i) {
+      const bool many = i == T_QFULL || (i >= T_CEMPTY && i < T_KEMPTY) || (i >= T_VFULL && i < T_VEMPTY) ||
+                        (i >= T_SCFULL && i < T_SFULL) || (i >= T_PFULL && i < T_PVDONE) || i >= T_XDONE;
+      mbar_init(&bars[i], many ? 128 : i == T_MMADONE ? 2 : 1);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (tid < 256) reinterpret_cast<float*>(sm + SM::MREF)[tid] = -INFINITY;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  const Q4Share share = q4_share<TQ_THREADS>(p, 128, TQ_MIN_STEPS, &start_s);   // has block barriers
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  auto wait = [&](int bar, uint32_t parity) {
+    if (*abort_flag) return;
+    if (!mbar_wait(&bars[bar], parity, kWaitLimitNs)) {
+      record_error(p.ws, PBSA_ERR_TIMEOUT, bar, K_Q4_ATTEND);
+      *abort_flag = 1;
+    }
+  };
+
+  if (warp < 4) {
+    setmaxnreg_dec<REG_CTRL>();
+    if (warp == 0) {
+      // ------------------------------------------------------------- slots' bytes
+      Q4Walk walk(p, share, 128);
+      int n = 0;   // step
+      bool stop = false;
+      while (!stop && walk.next()) {
+        const int* row = p.table + (size_t)walk.r * p.table_ld;
+        for (int b0 = walk.b0; b0 < walk.b1 && !stop; b0 += 32) {
+          const int mine = b0 + lane < walk.b1 ? __ldg(row + b0 + lane) : -1;
+          const int cnt = min(32, walk.b1 - b0);
+          for (int i = 0; i < cnt && !stop; i += 2) {
+            const int slot0 = __shfl_sync(0xffffffffu, mine, i), slot1 = __shfl_sync(0xffffffffu, mine, i + 1);
+            const int cs = n % CST;
+            if (lane == 0) {
+              wait(T_CEMPTY + cs, ((n / CST) & 1) ^ 1);
+              if (!*abort_flag) {
+                const bool has1 = i + 1 < cnt;
+                const bool ok0 = slot0 >= 0 && slot0 < p.pool_slots, ok1 = has1 && slot1 >= 0 && slot1 < p.pool_slots;
+                if (!ok0) record_error(p.ws, PBSA_ERR_DEVICE_INDEX, slot0, K_Q4_ATTEND);
+                if (has1 && !ok1) record_error(p.ws, PBSA_ERR_DEVICE_INDEX, slot1, K_Q4_ATTEND);
+                meta[2 * cs] = ok0;
+                meta[2 * cs + 1] = ok1;
+                uint8_t* dst = sm + SM::CODES + cs * SM::STEP;
+                const uint8_t* src = p.pool + (size_t)walk.h * p.pool_slots * Q::BYTES;
+                const uint32_t bytes = (ok0 ? Q::BYTES : 0) + (ok1 ? Q::BYTES : 0);
+                if (bytes > 0) mbar_arrive_expect_tx(&bars[T_CFULL + cs], bytes);
+                else mbar_arrive(&bars[T_CFULL + cs]);
+                if (ok0) bulk_load(dst, src + (size_t)slot0 * Q::BYTES, Q::BYTES, &bars[T_CFULL + cs]);
+                if (ok1) bulk_load(dst + Q::BYTES, src + (size_t)slot1 * Q::BYTES, Q::BYTES, &bars[T_CFULL + cs]);
+                ++n;
+              }
+            }
+            n = __shfl_sync(0xffffffffu, n, 0);
+            stop = __any_sync(0xffffffffu, *abort_flag != 0);
+          }
+        }
+      }
+      // the CTA must not end with copies in flight
+      if (lane == 0)
+        for (int i = max(0, n - CST); i < n; ++i) mbar_wait(&bars[T_CFULL + i % CST], (i / CST) & 1, kWaitLimitNs);
+      __syncwarp();
+    }
+    if (warp == 1 || warp == 3) {
+      // ------------------------------------------------------------- MMA issuers: steps of their parity
+      const uint32_t w = warp >> 1;
+      if (lane == 0) {
+        Q4Walk walk(p, share, 128);
+        const uint32_t tO = tmem + 384;
+        const uint64_t dq = sw128_desc(smem_u32(sm + SM::Q), 16, 1024);
+        const uint64_t dk = sw128_desc(smem_u32(sm + SM::K), 16, 1024);
+        const uint64_t dv = sw128_desc(smem_u32(sm + SM::V), 16384, 1024);
+        constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, 128, 0, 0), IDESC_PV = idesc_bf16_f32(128, D, 0, 1);
+        auto issue_qk = [&](int n) {
+          const int sk = n % KST, b = n % NSB;
+          wait(T_KFULL + sk, (n / KST) & 1);
+          if (*abort_flag) return;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+            mma_bf16_ss(tmem + b * 128, dq + off, dk + ((sk * SM::TILE) >> 4) + off, IDESC_QK, kk > 0 ? 1u : 0u);
+          }
+          mma_commit(&bars[T_SFULL + b]);
+          mma_commit(&bars[T_KEMPTY + sk]);
+        };
+        int n0 = 0, piece = 0;
+        while (walk.next()) {
+          if (walk.b0 == walk.b1) continue;
+          const int n1 = n0 + ((walk.b1 - walk.b0 + 1) >> 1);
+          wait(T_QFULL, piece & 1);
+          for (int n = n0 + ((n0 ^ (int)w) & 1); n < n1 && n < n0 + NSB; n += 2) issue_qk(n);
+          for (int n = n0 + ((n0 ^ (int)w) & 1); n < n1 && !*abort_flag; n += 2) {
+            const int sv = n % VST, b = n % NSB;
+            // PV(n-1) complete first, so that O accumulates in step order
+            if (n > n0) wait(T_PVDONE + ((n - 1) & 1), ((n - 1) >> 1) & 1);
+            wait(T_VFULL + sv, (n / VST) & 1);
+            wait(T_PFULL + b, (n / NSB) & 1);
+            if (*abort_flag) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              mma_bf16_ts(tO, tmem + b * 128 + kk * 8, dv + ((sv * SM::TILE + kk * 2048) >> 4), IDESC_PV,
+                          (n > n0 || kk > 0) ? 1u : 0u);
+            mma_commit(&bars[T_VEMPTY + sv]);
+            mma_commit(&bars[T_PVDONE + (n & 1)]);
+            if (n + NSB < n1) issue_qk(n + NSB);
+          }
+          // all MMAs of both issuers: the tile's O is complete, Q and the operand stages are free
+          mma_commit(&bars[T_MMADONE]);
+          mbar_wait(&bars[T_MMADONE], piece & 1, kWaitLimitNs);
+          n0 = n1;
+          ++piece;
+        }
+      }
+      __syncwarp();
+    }
+  } else if (warp < 8) {
+    setmaxnreg_dec<REG_UNPACK>();
+    // --------------------------------------------------------------- unpack
+    const int t = tid - 128, uw = warp - 4;
+    Q4Walk walk(p, share, 128);
+    int n = 0, piece = 0;
+    while (walk.next()) {
+      if (walk.b0 == walk.b1) continue;
+      // Q: one row a thread, and its sum
+      if (piece > 0) wait(T_MMADONE, (piece - 1) & 1);
+      {
+        const int rr = walk.mt * 128 + t;
+        const bool live = rr < walk.rows;
+        const int tok = live ? rr / p.group : 0, hd = live ? rr - tok * p.group : 0;
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
+                                                          (long long)(walk.q0 + tok) * p.q_ld +
+                                                          (long long)(walk.h * p.group + hd) * D);
+        float sum = 0.f;
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 v = live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum += lo_bf16(u[i]) + hi_bf16(u[i]);
+          *reinterpret_cast<uint4*>(sm + SM::Q + (c >> 3) * 16384 + t * 128 + (((c & 7) ^ (t & 7)) << 4)) = v;
+        }
+        reinterpret_cast<float*>(sm + SM::QS)[t] = sum;
+        fence_proxy_async_smem();
+        mbar_arrive(&bars[T_QFULL]);
+      }
+      for (int b = walk.b0; b < walk.b1; b += 2, ++n) {
+        const int cs = n % CST, sk = n % KST, sv = n % VST;
+        wait(T_CFULL + cs, (n / CST) & 1);
+        const uint8_t* codes = sm + SM::CODES + cs * SM::STEP;
+        const bool ok0 = meta[2 * cs] != 0, ok1 = meta[2 * cs + 1] != 0;
+        {   // scale and offset of key t, in log2 units
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + (t >> 6) * Q::BYTES + Q::OFF_KS + (t & 63) * 4);
+          float* sc = reinterpret_cast<float*>(sm + SM::SC) + (n % SCS) * 256;
+          const float s = lo_bf16(w);
+          sc[t] = s * p.scale_log2;
+          sc[128 + t] = fmaf(-128.f, s, hi_bf16(w)) * p.scale_log2;
+          if (t == 0) sc_ok[n % SCS] = (ok0 ? 1 : 0) | (ok1 ? 2 : 0);
+          mbar_arrive(&bars[T_SCFULL + n % SCS]);
+        }
+        wait(T_KEMPTY + sk, ((n / KST) & 1) ^ 1);
+        // K: 16 (D = 64: 8) code bytes a lane; 8 lanes write 4 rows of two neighbouring column groups, 8
+        // different 16-byte columns after the swizzle
+        {
+          constexpr int W = Q::WORDS;                   // words of a lane's bytes; 4 lanes a row
+          const int row8 = ((lane >> 4) & 1) * 4 + ((lane >> 1) & 3), j = ((lane >> 3) & 1) * 2 + (lane & 1);
+          uint8_t* dst = sm + SM::K + sk * SM::TILE;
+#pragma unroll
+          for (int it = 0; it < 4; ++it) {
+            const int row = uw * 32 + it * 8 + row8;    // key of the step
+            const uint8_t* src = codes + (row >> 6) * Q::BYTES + (row & 63) * Q::KROW + j * Q::LANE;
+            uint32_t w[W];
+            if (W == 4) {
+              const uint4 v = *reinterpret_cast<const uint4*>(src);
+              w[0] = v.x; w[1] = v.y; w[W - 2] = v.z; w[W - 1] = v.w;
+            } else {
+              const uint2 v = *reinterpret_cast<const uint2*>(src);
+              w[0] = v.x; w[1] = v.y;
+            }
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+              const int c = j * W + i;                  // 16-byte column
+              *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4)) =
+                  make_uint4(nibble_pair<0>(w[i]), nibble_pair<1>(w[i]), nibble_pair<2>(w[i]), nibble_pair<3>(w[i]));
+            }
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(&bars[T_KFULL + sk]);
+        }
+        wait(T_VEMPTY + sv, ((n / VST) & 1) ^ 1);
+        // V: 8 channels of two tokens a lane
+        {
+          constexpr int HALVES = D / 64;                // 8-channel halves of a lane's bytes in the layout
+          constexpr int PER = 8 * 4 * HALVES;           // tasks of 8 tokens
+          uint8_t* dst = sm + SM::V + sv * SM::TILE;
+          const int left = walk.kv_len - b * BT;        // tokens of this step that are cached
+#pragma unroll 2
+          for (int e = t; e < 16 * PER; e += 128) {
+            const int k = e % HALVES, j = (e / HALVES) & 3, g = (e / (HALVES * 4)) & 7, u8 = e / PER;
+            const int row = u8 * 8 + 2 * j;             // of the step's 128 keys
+            const uint8_t* blk = codes + (row >> 6) * Q::BYTES;
+            const uint2 w = *reinterpret_cast<const uint2*>(blk + Q::OFF_V + ((u8 & 7) * 32 + g * 4 + j) * Q::LANE + 8 * k);
+            uint2 sc = *reinterpret_cast<const uint2*>(blk + Q::OFF_VS + (row & 63) * 4);
+            const bool ok = row < 64 ? ok0 : ok1;
+            if (!ok || row >= left) sc.x = 0u;
+            if (!ok || row + 1 >= left) sc.y = 0u;
+            const uint32_t s0 = __byte_perm(sc.x, 0, 0x1010), m0 = __byte_perm(sc.x, 0, 0x3232);
+            const uint32_t s1 = __byte_perm(sc.y, 0, 0x1010), m1 = __byte_perm(sc.y, 0, 0x3232);
+            uint32_t x[8] = {nibble_pair<0>(w.x), nibble_pair<1>(w.x), nibble_pair<2>(w.x), nibble_pair<3>(w.x),
+                             nibble_pair<0>(w.y), nibble_pair<1>(w.y), nibble_pair<2>(w.y), nibble_pair<3>(w.y)};
+            uint32_t a[4], c[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t lo = sub_bf16x2(x[2 * i], 0x43004300u), hi = sub_bf16x2(x[2 * i + 1], 0x43004300u);
+              a[i] = fma_bf16x2(__byte_perm(lo, hi, 0x5410), s0, m0);
+              c[i] = fma_bf16x2(__byte_perm(lo, hi, 0x7632), s1, m1);
+            }
+            const int col = g * HALVES + k;
+            uint8_t* at = dst + (col >> 3) * 16384;
+            *reinterpret_cast<uint4*>(at + row * 128 + (((col & 7) ^ (row & 7)) << 4)) = make_uint4(a[0], a[1], a[2], a[3]);
+            *reinterpret_cast<uint4*>(at + (row + 1) * 128 + (((col & 7) ^ ((row + 1) & 7)) << 4)) =
+                make_uint4(c[0], c[1], c[2], c[3]);
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(&bars[T_VFULL + sv]);
+        }
+        mbar_arrive(&bars[T_CEMPTY + cs]);
+      }
+      ++piece;
+    }
+  } else {
+    setmaxnreg_inc<REG_SOFT>();
+    // --------------------------------------------------------------- softmax
+    const int wg = (warp - 8) >> 2;          // steps of this parity
+    const int wq = warp & 3;                 // TMEM lane quadrant this warp may access
+    const int row = wq * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
+    const uint32_t tO = tmem + lane_off + 384;
+    float* mref2 = reinterpret_cast<float*>(sm + SM::MREF);
+    Q4Walk walk(p, share, 128);
+    int n0 = 0, piece = 0;
+    while (walk.next()) {
+      const int n1 = n0 + ((walk.b1 - walk.b0 + 1) >> 1);
+      const int rr = walk.mt * 128 + row;
+      const bool live = rr < walk.rows;
+      if (walk.b0 == walk.b1) {   // nothing to see: no other role takes part
+        if (wg == 0 && live) {
+          const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int ch = 0; ch < D; ch += 4) {
+            if (walk.piece < 0)
+              q4_write_row<D>(p, walk.q0, rr, walk.h, ch, zero, -INFINITY, 0.f, ch == 0);
+            else
+              *reinterpret_cast<float4*>(p.part_o + ((size_t)walk.piece * p.part_rows + row) * D + ch) =
+                  make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+          if (walk.piece >= 0) p.part_ml[(size_t)walk.piece * p.part_rows + row] = make_float2(-INFINITY, 0.f);
+        }
+        continue;
+      }
+      const int lim = live && p.causal ? max(walk.kv_len - walk.q_len + rr / p.group + 1, 0) : walk.kv_len;
+      float* mref = mref2 + (piece & 1) * 128;
+      wait(T_QFULL, piece & 1);
+      const float qs = reinterpret_cast<const float*>(sm + SM::QS)[row];
+      // O has one reference maximum per row, shared by both warpgroups; l is this one's share of the
+      // row's sum, against the reference m it last used.
+      float m = -INFINITY, l = 0.f;
+      for (int n = n0 + ((n0 ^ wg) & 1); n < n1; n += 2) {
+        const int b = n % NSB;
+        const uint32_t tS = tmem + lane_off + b * 128;
+        wait(T_SCFULL + n % SCS, (n / SCS) & 1);
+        const float4* s4 = reinterpret_cast<const float4*>(sm + SM::SC) + (n % SCS) * 64;
+        const int ok = sc_ok[n % SCS];
+        wait(T_SFULL + b, (n / NSB) & 1);
+        if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+        tc_fence_after();
+        uint32_t x[4][32];
+        tmem_ld32(tS + 0, x[0]);
+        tmem_ld32(tS + 32, x[1]);
+        tmem_wait_ld();
+        tmem_ld32(tS + 64, x[2]);
+        tmem_ld32(tS + 96, x[3]);
+        const int see = lim - (walk.b0 + 2 * (n - n0)) * BT;    // of the step's keys
+        const bool cut = __any_sync(0xffffffffu, see < 128) || ok != 3;
+        float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (q == 2) tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 s = s4[q * 8 + e / 4], o = s4[32 + q * 8 + e / 4];
+            float y0, y1, y2, y3, o0, o1, o2, o3;
+            fmul2(o.x, o.y, qs, qs, o0, o1);
+            fmul2(o.z, o.w, qs, qs, o2, o3);
+            fma2(__uint_as_float(x[q][e]), __uint_as_float(x[q][e + 1]), s.x, s.y, o0, o1, y0, y1);
+            fma2(__uint_as_float(x[q][e + 2]), __uint_as_float(x[q][e + 3]), s.z, s.w, o2, o3, y2, y3);
+            if (cut) {
+              const bool okb = (ok >> (q >> 1)) & 1;
+              if (!okb || q * 32 + e >= see) y0 = -INFINITY;
+              if (!okb || q * 32 + e + 1 >= see) y1 = -INFINITY;
+              if (!okb || q * 32 + e + 2 >= see) y2 = -INFINITY;
+              if (!okb || q * 32 + e + 3 >= see) y3 = -INFINITY;
+            }
+            mx0 = fmax3(mx0, y0, y1);
+            mx1 = fmax3(mx1, y2, y3);
+            x[q][e] = __float_as_uint(y0);
+            x[q][e + 1] = __float_as_uint(y1);
+            x[q][e + 2] = __float_as_uint(y2);
+            x[q][e + 3] = __float_as_uint(y3);
+          }
+        }
+        const float mb = fmaxf(mx0, mx1);
+        // the warpgroups take turns on the exponentials; the hand-off carries the reference maximum
+        if (n > n0) wait(T_XDONE + (wg ^ 1), ((n - 1) >> 1) & 1);
+        float alpha = 1.f;
+        {
+          const float mcur = mref[row];
+          float mn = mcur;
+          if (mb > mcur + 8.0f) {
+            if (mcur != -INFINITY) alpha = ex2_approx(mcur - mb);
+            mn = mb;
+          }
+          mref[row] = mn;
+          if (mn != m) {
+            if (m != -INFINITY) l *= ex2_approx(m - mn);
+            m = mn;
+          }
+        }
+        const float neg = m == -INFINITY ? 0.f : -m;     // (a row that has seen no key: -inf stays -inf)
+        float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float a0 = neg, a1 = neg;
+            fadd2(a0, a1, __uint_as_float(x[q][2 * e]), __uint_as_float(x[q][2 * e + 1]));
+            const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);
+            if (e & 1) fadd2(ls[2], ls[3], p0, p1);
+            else fadd2(ls[0], ls[1], p0, p1);
+            pk[e] = pack_bf16(p0, p1);
+          }
+          tmem_st16(tS + q * 16, pk);
+        }
+        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        mbar_arrive(&bars[T_XDONE + wg]);
+        if (__any_sync(0xffffffffu, alpha != 1.f)) {     // tcgen05.ld/st are warp-collective
+          wait(T_PVDONE + ((n - 1) & 1), ((n - 1) >> 1) & 1);
+          tc_fence_after();
+#pragma unroll 1
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t ov[32];
+            tmem_ld32(tO + q * 32, ov);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+            tmem_st32(tO + q * 32, ov);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bars[T_PFULL + b]);
+      }
+      // ------------------------------------------------------------- the piece's end
+      wait(T_MMADONE, piece & 1);
+      float2* stat = reinterpret_cast<float2*>(sm + SM::STAT);
+      stat[wg * 128 + row] = make_float2(m, l);
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      const float2 st0 = stat[row], st1 = stat[128 + row];
+      const float M = mref[row];
+      const float L = st0.y * q4_weight(st0.x, M) + st1.y * q4_weight(st1.x, M);
+      tc_fence_after();
+#pragma unroll 1
+      for (int q = 0; q < D / 64; ++q) {                 // this warpgroup's half of the channels
+        const int ch = wg * (D / 2) + q * 32;
+        uint32_t ov[32];
+        tmem_ld32(tO + ch, ov);
+        tmem_wait_ld();
+        if (live && !*abort_flag) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float acc[4] = {__uint_as_float(ov[e]), __uint_as_float(ov[e + 1]), __uint_as_float(ov[e + 2]),
+                                  __uint_as_float(ov[e + 3])};
+            if (walk.piece < 0)
+              q4_write_row<D>(p, walk.q0, rr, walk.h, ch + e, acc, M, L, ch + e == 0);
+            else
+              *reinterpret_cast<float4*>(p.part_o + ((size_t)walk.piece * p.part_rows + row) * D + ch + e) =
+                  make_float4(acc[0], acc[1], acc[2], acc[3]);
+          }
+        }
+      }
+      if (wg == 0) {
+        if (walk.piece >= 0 && live && !*abort_flag) p.part_ml[(size_t)walk.piece * p.part_rows + row] = make_float2(M, L);
+        mref2[((piece & 1) ^ 1) * 128 + row] = -INFINITY;   // the next piece's
+      }
+      tc_fence_before();
+      asm volatile("bar.sync 1, 256;" ::: "memory");      // O, the statistics and the references are free
+      n0 = n1;
+      ++piece;
+    }
+    if (tid == 256) p.desc[blockIdx.x] = walk.desc;
+  }
+
+  // ----------------------------------------------------------------- teardown
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+cudaError_t launch_t(AttendQ4Params p, cudaStream_t st) {
+  auto kern = attend_q4_tc_kernel<D>;
+  cudaError_t e = set_smem_once((const void*)kern, (int)TqSmem<D>::BYTES);
+  if (e != cudaSuccess) return e;
+  p.part_rows = 128;
+  int sms = 0, dev = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  const int grid = sms < Q4_TC_MAX_CTAS ? sms : Q4_TC_MAX_CTAS;
+  kern<<<grid, TQ_THREADS, TqSmem<D>::BYTES, st>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return launch_q4_join<D>(p, grid, 8, st);
+}
+
+}  // namespace
+
+cudaError_t launch_attend_q4_tc(AttendQ4Params p, int d, cudaStream_t st) {
+  return d == 128 ? launch_t<128>(p, st) : launch_t<64>(p, st);
+}
+
+}  // namespace pbsa

@@ -239,6 +239,37 @@ def test_prompts_and_decodes_together(hq, hk, d, dtype, causal):
     f.check(*f.attend(causal), causal)
 
 
+@pytest.mark.parametrize("lens,hq,hk,d,causal", [
+    ([(700, 0)], 4, 2, 128, True),                     # a prompt from nothing: row tiles see more and more
+    ([(300, 1500), (1, 90), (40, 0), (257, 31)], 6, 2, 128, True),
+    ([(130, 2000), (129, 63)], 8, 8, 64, False),
+    ([(33, 5000)], 1, 1, 128, True),                   # one row tile over every CTA
+    ([(513, 700), (0, 3), (2, 4000)], 3, 1, 64, True),
+    ([(5, 333), (4, 100)], 64, 1, 128, True),          # 64 heads share one
+])
+def test_long_prompts(lens, hq, hk, d, causal):
+    f = Filled(lens, hq, hk, d, "bf16", seed=14, rows_after=2)
+    f.check(*f.attend(causal), causal)
+
+
+def test_tiles_without_keys_among_others():
+    """Prompts of which only a few tokens are cached: whole row tiles see nothing, in the middle of a CTA's share
+    and at its ends."""
+    lens = [(200, 0), (140, 60), (300, 0), (200, 100)]
+    f = Filled(lens, 4, 1, 128, "bf16", seed=15)
+    full = f.kv_len.clone()
+    f.kv_len[0] = 3
+    f.kv_len[2] = 0
+    o, lse = f.attend(True)
+    assert P.pbsa_get_device_error(f.ws) == 0
+    assert (o[:197] == 0).all() and torch.isneginf(lse[:, :197]).all() and torch.isfinite(lse[:, 197:200]).all()
+    assert (o[340:640] == 0).all() and torch.isneginf(lse[:, 340:640]).all()
+    f.kv_len = full
+    want, wl = f.attend(True)
+    assert torch.equal(o[200:340], want[200:340]) or (o[200:340] - want[200:340]).abs().max() <= 2.0 ** -6
+    f.check(want, wl, True)
+
+
 def test_long_cache_is_split_and_joined():
     """One request over hundreds of blocks (every CTA holds a piece), and beside short ones."""
     for lens in ([(1, 40000)], [(1, 3), (1, 20000), (2, 64), (1, 9000)]):
