@@ -13,9 +13,11 @@
 //      x = s (q . (c + 128)) + (m - 128 s) sum(q),
 //    so they carry no rounding of K; rounding K to bf16 would put 2^-8 |q . k| / sqrt(d) of noise into each.
 //  * TMEM: three S/P buffers and one O accumulator (512 columns), two softmax warpgroups on alternate
-//    steps, two MMA-issuing threads, P over S as bf16, O rescaled only when the reference maximum grows
-//    by more than 2^8.  S(i+3) is issued behind PV(i), so a warpgroup never waits for its own PV.
-//    (pbsa_attend is paced the same way.)
+//    steps, two MMA-issuing threads, P over S as bf16.  S(i+3) is issued behind PV(i), so a warpgroup never
+//    waits for its own PV.  The softmax makes one pass over a step's scores: scale, exponential, sum and
+//    maximum together, against the reference that the steps before left.  A step whose maximum exceeds it
+//    by 2^8 moves the reference for the next one (O is rescaled then); P of the step itself may be as large as
+//    2^64, above which the pass is done again.
 //  * All barriers are used once per step with a step count that runs on over the pieces (a piece without
 //    blocks takes part in none).  The ring of key scales has four places: the unpackers reach step n only when
 //    PV(n-3), and so the softmax of step n-3, is done.
@@ -52,14 +54,18 @@ struct TqSmem {
   static constexpr uint32_t CODES = V + VST * TILE;
   static constexpr uint32_t SC = CODES + CST * STEP;                // float [SCS][2][128]: per key, scale and offset
   static constexpr uint32_t QS = SC + SCS * 1024;                   // float [128]: sums of the rows of Q
-  static constexpr uint32_t MREF = QS + 512;                        // float [2][128]
-  static constexpr uint32_t STAT = MREF + 1024;                     // float2 [2][128]
+  static constexpr uint32_t MREF = QS + 512;                        // float2 [128]
+  static constexpr uint32_t RLAST = MREF + 1024;                    // float [128]
+  static constexpr uint32_t STAT = RLAST + 512;                     // float2 [2][128]
   static constexpr uint32_t BARS = STAT + 2048;
   static constexpr uint32_t META = BARS + T_BARS * 8;               // int [CST][2], int [SCS], TMEM address, abort flag
   static constexpr uint32_t TOTAL = META + 4 * (2 * CST + SCS + 2);
   static constexpr uint32_t BYTES = TOTAL + 1024;
 };
 static_assert(TqSmem<128>::BYTES <= 232448, "shared memory");
+
+struct Yes { static constexpr bool value = true; };
+struct No { static constexpr bool value = false; };
 
 __device__ __forceinline__ void fma2(float x0, float x1, float y0, float y1, float z0, float z1, float& d0, float& d1) {
   asm("{\n\t.reg .b64 x, y, z, d;\n\t"
@@ -101,7 +107,6 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (tid < 256) reinterpret_cast<float*>(sm + SM::MREF)[tid] = -INFINITY;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == 1) {
     tmem_alloc(tmem_holder, 512);
@@ -339,7 +344,7 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
     const int row = wq * 32 + lane;
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const uint32_t tO = tmem + lane_off + 384;
-    float* mref2 = reinterpret_cast<float*>(sm + SM::MREF);
+    float2* mref = reinterpret_cast<float2*>(sm + SM::MREF);   // (reference of the next step, factor to it)
     Q4Walk walk(p, share, 128);
     int n0 = 0, piece = 0;
     while (walk.next()) {
@@ -361,11 +366,11 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
         continue;
       }
       const int lim = live && p.causal ? max(walk.kv_len - walk.q_len + rr / p.group + 1, 0) : walk.kv_len;
-      float* mref = mref2 + (piece & 1) * 128;
       wait(T_QFULL, piece & 1);
       const float qs = reinterpret_cast<const float*>(sm + SM::QS)[row];
-      // O has one reference maximum per row, shared by both warpgroups; l is this one's share of the
-      // row's sum, against the reference m it last used.
+      // A row has one reference for O and every l, handed from step to step with the factor that takes
+      // what was summed before to it.  l is this warpgroup's share of the row's sum, against the reference
+      // m it last used.
       float m = -INFINITY, l = 0.f;
       for (int n = n0 + ((n0 ^ wg) & 1); n < n1; n += 2) {
         const int b = n % NSB;
@@ -379,74 +384,88 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
         uint32_t x[4][32];
         tmem_ld32(tS + 0, x[0]);
         tmem_ld32(tS + 32, x[1]);
-        tmem_wait_ld();
         tmem_ld32(tS + 64, x[2]);
         tmem_ld32(tS + 96, x[3]);
+        tmem_wait_ld();
         const int see = lim - (walk.b0 + 2 * (n - n0)) * BT;    // of the step's keys
         const bool cut = __any_sync(0xffffffffu, see < 128) || ok != 3;
-        float mx0 = -INFINITY, mx1 = -INFINITY;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (q == 2) tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 s = s4[q * 8 + e / 4], o = s4[32 + q * 8 + e / 4];
-            float y0, y1, y2, y3, o0, o1, o2, o3;
-            fmul2(o.x, o.y, qs, qs, o0, o1);
-            fmul2(o.z, o.w, qs, qs, o2, o3);
-            fma2(__uint_as_float(x[q][e]), __uint_as_float(x[q][e + 1]), s.x, s.y, o0, o1, y0, y1);
-            fma2(__uint_as_float(x[q][e + 2]), __uint_as_float(x[q][e + 3]), s.z, s.w, o2, o3, y2, y3);
-            if (cut) {
-              const bool okb = (ok >> (q >> 1)) & 1;
-              if (!okb || q * 32 + e >= see) y0 = -INFINITY;
-              if (!okb || q * 32 + e + 1 >= see) y1 = -INFINITY;
-              if (!okb || q * 32 + e + 2 >= see) y2 = -INFINITY;
-              if (!okb || q * 32 + e + 3 >= see) y3 = -INFINITY;
-            }
-            mx0 = fmax3(mx0, y0, y1);
-            mx1 = fmax3(mx1, y2, y3);
-            x[q][e] = __float_as_uint(y0);
-            x[q][e + 1] = __float_as_uint(y1);
-            x[q][e + 2] = __float_as_uint(y2);
-            x[q][e + 3] = __float_as_uint(y3);
-          }
-        }
-        const float mb = fmaxf(mx0, mx1);
-        // the warpgroups take turns on the exponentials; the hand-off carries the reference maximum
+        // the warpgroups take turns on the exponentials; the hand-off carries the reference
         if (n > n0) wait(T_XDONE + (wg ^ 1), ((n - 1) >> 1) & 1);
-        float alpha = 1.f;
+        float R = -INFINITY, alpha = 1.f, neg, mx, ls[4];
+        if (n > n0) {
+          const float2 v = mref[row];
+          R = v.x;
+          alpha = v.y;
+        }
+        // P = 2^(x - R) over S as bf16 pairs, its row sum, and the maximum of x - R (plain: R enters the fused
+        // product, whose rounding is far below 1 then) or of x (careful: x first, so that its maximum less
+        // itself is zero however large it is; masked keys)
+        auto pass = [&](auto careful) {
+          mx = -INFINITY;
+          float mx1 = -INFINITY;
+          ls[0] = ls[1] = ls[2] = ls[3] = 0.f;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const float4 s = s4[q * 8 + e / 4], o = s4[32 + q * 8 + e / 4];
+              float y0, y1, y2, y3, o0, o1, o2, o3;
+              const float off = decltype(careful)::value ? 0.f : neg;
+              ffma2(o.x, o.y, qs, off, o0, o1);
+              ffma2(o.z, o.w, qs, off, o2, o3);
+              fma2(__uint_as_float(x[q][e]), __uint_as_float(x[q][e + 1]), s.x, s.y, o0, o1, y0, y1);
+              fma2(__uint_as_float(x[q][e + 2]), __uint_as_float(x[q][e + 3]), s.z, s.w, o2, o3, y2, y3);
+              if (decltype(careful)::value) {
+                const int to = (ok >> (q >> 1)) & 1 ? see - q * 32 - e : 0;
+                if (to <= 0) y0 = -INFINITY;
+                if (to <= 1) y1 = -INFINITY;
+                if (to <= 2) y2 = -INFINITY;
+                if (to <= 3) y3 = -INFINITY;
+              }
+              mx = fmax3(mx, y0, y1);
+              mx1 = fmax3(mx1, y2, y3);
+              if (decltype(careful)::value) { y0 += neg; y1 += neg; y2 += neg; y3 += neg; }
+              y0 = ex2_approx(y0);
+              y1 = ex2_approx(y1);
+              y2 = ex2_approx(y2);
+              y3 = ex2_approx(y3);
+              fadd2(ls[0], ls[1], y0, y1);
+              fadd2(ls[2], ls[3], y2, y3);
+              pk[e / 2] = pack_bf16(y0, y1);
+              pk[e / 2 + 1] = pack_bf16(y2, y3);
+            }
+            tmem_st16(tS + q * 16, pk);
+          }
+          mx = fmaxf(mx, mx1);
+        };
+        // Scores may exceed the reference: P up to 2^64 fits its type, and the next step's reference follows.
+        // Above that, and where no key has been seen yet, the pass is done again against the row's maximum.
+        // (Twice at the most: a maximum found by a plain pass may be rounded, a careful one's is not.)
+#pragma unroll 1
+        for (int turn = 0;; ++turn) {
+          neg = R == -INFINITY ? 0.f : -R;
+          const bool careful = cut || __any_sync(0xffffffffu, fabsf(neg) > 4096.f);
+          if (careful) pass(Yes{});
+          else pass(No{});
+          const float top = careful ? mx : mx - neg;       // the row's maximum of x in this step
+          if (careful) mx = mx + neg;
+          const bool again = R == -INFINITY ? top > -INFINITY : mx > 64.f;
+          if (turn == 3 || !__any_sync(0xffffffffu, again)) break;
+          if (again) {
+            if (R != -INFINITY) alpha *= ex2_approx(-mx);
+            R = top;
+          }
+        }
         {
-          const float mcur = mref[row];
-          float mn = mcur;
-          if (mb > mcur + 8.0f) {
-            if (mcur != -INFINITY) alpha = ex2_approx(mcur - mb);
-            mn = mb;
-          }
-          mref[row] = mn;
-          if (mn != m) {
-            if (m != -INFINITY) l *= ex2_approx(m - mn);
-            m = mn;
-          }
+          const bool grow = mx > 8.f && R != -INFINITY;
+          mref[row] = grow ? make_float2(R + mx, ex2_approx(-mx)) : make_float2(R, 1.f);
         }
-        const float neg = m == -INFINITY ? 0.f : -m;     // (a row that has seen no key: -inf stays -inf)
-        float ls[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float a0 = neg, a1 = neg;
-            fadd2(a0, a1, __uint_as_float(x[q][2 * e]), __uint_as_float(x[q][2 * e + 1]));
-            const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);
-            if (e & 1) fadd2(ls[2], ls[3], p0, p1);
-            else fadd2(ls[0], ls[1], p0, p1);
-            pk[e] = pack_bf16(p0, p1);
-          }
-          tmem_st16(tS + q * 16, pk);
-        }
-        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
         mbar_arrive(&bars[T_XDONE + wg]);
-        if (__any_sync(0xffffffffu, alpha != 1.f)) {     // tcgen05.ld/st are warp-collective
+        if (m != -INFINITY && m != R) l *= ex2_approx(m - R);
+        m = R;
+        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        if (n > n0 && __any_sync(0xffffffffu, alpha != 1.f)) {     // tcgen05.ld/st are warp-collective
           wait(T_PVDONE + ((n - 1) & 1), ((n - 1) >> 1) & 1);
           tc_fence_after();
 #pragma unroll 1
@@ -462,6 +481,7 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&bars[T_PFULL + b]);
+        if (n + 1 == n1) reinterpret_cast<float*>(sm + SM::RLAST)[row] = R;   // what O is against
       }
       // ------------------------------------------------------------- the piece's end
       wait(T_MMADONE, piece & 1);
@@ -469,7 +489,7 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
       stat[wg * 128 + row] = make_float2(m, l);
       asm volatile("bar.sync 1, 256;" ::: "memory");
       const float2 st0 = stat[row], st1 = stat[128 + row];
-      const float M = mref[row];
+      const float M = reinterpret_cast<const float*>(sm + SM::RLAST)[row];
       const float L = st0.y * q4_weight(st0.x, M) + st1.y * q4_weight(st1.x, M);
       tc_fence_after();
 #pragma unroll 1
@@ -491,10 +511,8 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
           }
         }
       }
-      if (wg == 0) {
-        if (walk.piece >= 0 && live && !*abort_flag) p.part_ml[(size_t)walk.piece * p.part_rows + row] = make_float2(M, L);
-        mref2[((piece & 1) ^ 1) * 128 + row] = -INFINITY;   // the next piece's
-      }
+      if (wg == 0 && walk.piece >= 0 && live && !*abort_flag)
+        p.part_ml[(size_t)walk.piece * p.part_rows + row] = make_float2(M, L);
       tc_fence_before();
       asm volatile("bar.sync 1, 256;" ::: "memory");      // O, the statistics and the references are free
       n0 = n1;

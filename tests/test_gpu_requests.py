@@ -293,6 +293,38 @@ def test_rows_without_keys():
     assert (o[5:] == 0).all() and torch.isneginf(lse[:, 5:]).all() and torch.isfinite(lse[:, :5]).all()
 
 
+@pytest.mark.parametrize("lens", [[(1, 700), (4, 300)], [(40, 900), (130, 300)]])
+@pytest.mark.parametrize("factor", [30.0, 1e4, 1e9, 1e20, 1e34])
+def test_large_scores(lens, factor):
+    """Scores from hundreds to the end of fp32's range: the softmax picks one key, whose value is the output (where
+    two keys' scores are nearer than fp32 can tell, any mix of theirs), and nothing overflows."""
+    f = Filled(lens, 4, 2, 128, "bf16", seed=16, q_scale=factor)
+    o, lse = f.attend(True)
+    assert P.pbsa_get_device_error(f.ws) == 0
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+    at = kv = 0
+    q, k, v = (t.double().numpy() for t in (f.q, f.k, f.v))
+    for n, p in lens:
+        kk, vv = RO.held(k[kv:kv + n + p], v[kv:kv + n + p])
+        for i in range(n):
+            for h in range(4):
+                L = p + i + 1
+                z = 128 ** -0.5 * (kk[:L, h // 2] @ q[at + i, h])
+                # a score's error as in Filled._bounds: 2^-18 of the products it sums, the codes' offset included
+                _, ks, km = RO.quantise(k[kv:kv + L, h // 2])
+                dx = 2.0 ** -18 * 128 ** -0.5 * (136.0 * ks.max() * np.abs(q[at + i, h]).sum()
+                                                 + np.abs(km).max() * abs(q[at + i, h].sum()))
+                near = z >= z.max() - 2.0 * dx - 30.0        # (e^-30 of the largest weight and less is nothing)
+                lo, hi = vv[:L, h // 2][near].min(0), vv[:L, h // 2][near].max(0)
+                got = o[at + i, h].double().cpu().numpy()
+                slack = 2.0 ** -6 * np.abs(vv).max()
+                assert (got >= lo - slack).all() and (got <= hi + slack).all()
+                # log of a sum of at most L weights, in fp32
+                assert abs(float(lse[h, at + i]) - z.max()) <= dx + np.log(L) + 2.0 ** -20 * abs(z.max()) + 1e-3
+        at += n
+        kv += n + p
+
+
 @pytest.mark.parametrize("lens", [[(1, 70), (1, 100)], [(40, 50), (130, 5)]])
 def test_values_that_are_not_finite_reach_only_the_rows_that_see_them(lens):
     """A token that is not finite makes the rows that attend it NaN, and no others: not those it is masked for
