@@ -15,9 +15,10 @@
 //  * TMEM: three S/P buffers and one O accumulator (512 columns), two softmax warpgroups on alternate
 //    steps, two MMA-issuing threads, P over S as bf16.  S(i+3) is issued behind PV(i), so a warpgroup never
 //    waits for its own PV.  The softmax makes one pass over a step's scores: scale, exponential, sum and
-//    maximum together, against the reference that the steps before left.  A step whose maximum exceeds it
-//    by 2^8 moves the reference for the next one (O is rescaled then); P of the step itself may be as large as
-//    2^64, above which the pass is done again.
+//    maximum together, against the reference that the steps before the last one left, so the two warpgroups'
+//    passes overlap.  A step whose maximum exceeds it by 2^8 moves the reference for a later one (O is
+//    rescaled then).  P of the step itself may be as large as 2^100; where a bound on its scores does not
+//    promise that, their maximum is found first.
 //  * All barriers are used once per step with a step count that runs on over the pieces (a piece without
 //    blocks takes part in none).  The ring of key scales has four places: the unpackers reach step n only when
 //    PV(n-3), and so the softmax of step n-3, is done.
@@ -41,7 +42,13 @@ static_assert(REG_CTRL + REG_UNPACK + 2 * REG_SOFT <= 4 * 128, "register split e
 enum { T_QFULL = 0, T_CFULL = 1, T_CEMPTY = T_CFULL + CST, T_KFULL = T_CEMPTY + CST, T_KEMPTY = T_KFULL + KST,
        T_VFULL = T_KEMPTY + KST, T_VEMPTY = T_VFULL + VST, T_SCFULL = T_VEMPTY + VST, T_SFULL = T_SCFULL + SCS,
        T_PFULL = T_SFULL + NSB, T_PVDONE = T_PFULL + NSB, T_MMADONE = T_PVDONE + 2, T_XDONE = T_MMADONE + 1,
-       T_BARS = T_XDONE + 2 };
+       T_WFULL = T_XDONE + 2, T_WEMPTY = T_WFULL + 2, T_BARS = T_WEMPTY + 2 };
+constexpr int WARPS_TOLD = 15;       // warps that read the pieces: all but the one that walks them
+
+// A piece of the CTA's share, as the walking warp passes it on.
+struct TqPiece {
+  int more, r, b0, b1, mt, h, q0, q_len, kv_len, rows, piece, pad;
+};
 
 template <int D>
 struct TqSmem {
@@ -53,19 +60,19 @@ struct TqSmem {
   static constexpr uint32_t V = K + KST * TILE;
   static constexpr uint32_t CODES = V + VST * TILE;
   static constexpr uint32_t SC = CODES + CST * STEP;                // float [SCS][2][128]: per key, scale and offset
-  static constexpr uint32_t QS = SC + SCS * 1024;                   // float [128]: sums of the rows of Q
-  static constexpr uint32_t MREF = QS + 512;                        // float2 [128]
+  static constexpr uint32_t KB = SC + SCS * 1024;                   // float [SCS][4]: the largest |key channel| of 32 keys
+  static constexpr uint32_t QS = KB + SCS * 16;                     // float [2][128]: sums of the rows of Q, of |Q|
+  static constexpr uint32_t MREF = QS + 1024;                       // float2 [128]
   static constexpr uint32_t RLAST = MREF + 1024;                    // float [128]
   static constexpr uint32_t STAT = RLAST + 512;                     // float2 [2][128]
-  static constexpr uint32_t BARS = STAT + 2048;
-  static constexpr uint32_t META = BARS + T_BARS * 8;               // int [CST][2], int [SCS], TMEM address, abort flag
+  static constexpr uint32_t IDENT = STAT + 2048;                    // float [2][128]: a scale of 1, an offset of 0
+  static constexpr uint32_t BARS = IDENT + 1024;
+  static constexpr uint32_t WALK = BARS + T_BARS * 8;               // TqPiece [2]
+  static constexpr uint32_t META = WALK + 2 * sizeof(TqPiece);      // int [CST][2], int [SCS], TMEM address, abort flag
   static constexpr uint32_t TOTAL = META + 4 * (2 * CST + SCS + 2);
   static constexpr uint32_t BYTES = TOTAL + 1024;
 };
 static_assert(TqSmem<128>::BYTES <= 232448, "shared memory");
-
-struct Yes { static constexpr bool value = true; };
-struct No { static constexpr bool value = false; };
 
 __device__ __forceinline__ void fma2(float x0, float x1, float y0, float y1, float z0, float z1, float& d0, float& d1) {
   asm("{\n\t.reg .b64 x, y, z, d;\n\t"
@@ -101,12 +108,13 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
   if (tid == 0) {
     for (int i = 0; i < T_BARS; ++i) {
       const bool many = i == T_QFULL || (i >= T_CEMPTY && i < T_KEMPTY) || (i >= T_VFULL && i < T_VEMPTY) ||
-                        (i >= T_SCFULL && i < T_SFULL) || (i >= T_PFULL && i < T_PVDONE) || i >= T_XDONE;
-      mbar_init(&bars[i], many ? 128 : i == T_MMADONE ? 2 : 1);
+                        (i >= T_SCFULL && i < T_SFULL) || (i >= T_PFULL && i < T_PVDONE) || (i >= T_XDONE && i < T_WFULL);
+      mbar_init(&bars[i], many ? 128 : i == T_MMADONE ? 2 : i >= T_WEMPTY ? WARPS_TOLD : 1);
     }
     *abort_flag = 0;
     fence_barrier_init();
   }
+  if (tid < 256) reinterpret_cast<float*>(sm + SM::IDENT)[tid] = tid < 128 ? 1.f : 0.f;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == 1) {
     tmem_alloc(tmem_holder, 512);
@@ -124,14 +132,40 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
     }
   };
 
+  // The k-th piece, for a whole warp (not cut short by an abort: every role goes through every piece).
+  auto told = [&](int k) {
+    if (!mbar_wait(&bars[T_WFULL + (k & 1)], (k >> 1) & 1, 2 * kWaitLimitNs)) *abort_flag = 1;
+    const TqPiece w = reinterpret_cast<const TqPiece*>(sm + SM::WALK)[k & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars[T_WEMPTY + (k & 1)]);
+    return w;
+  };
+
   if (warp < 4) {
     setmaxnreg_dec<REG_CTRL>();
+    if (warp == 2) {
+      // ------------------------------------------------------------- walks the share
+      if (lane == 0) {
+        Q4Walk walk(p, share, 128);
+        bool more = true;
+        for (int k = 0; more; ++k) {
+          more = walk.next();
+          if (!mbar_wait(&bars[T_WEMPTY + (k & 1)], ((k >> 1) & 1) ^ 1, 2 * kWaitLimitNs)) *abort_flag = 1;
+          reinterpret_cast<TqPiece*>(sm + SM::WALK)[k & 1] = {more ? 1 : 0, walk.r, walk.b0, walk.b1, walk.mt, walk.h,
+                                                             walk.q0, walk.q_len, walk.kv_len, walk.rows, walk.piece, 0};
+          mbar_arrive(&bars[T_WFULL + (k & 1)]);
+        }
+        p.desc[blockIdx.x] = walk.desc;
+      }
+      __syncwarp();
+    }
     if (warp == 0) {
       // ------------------------------------------------------------- slots' bytes
-      Q4Walk walk(p, share, 128);
       int n = 0;   // step
       bool stop = false;
-      while (!stop && walk.next()) {
+      for (int k = 0;; ++k) {
+        const TqPiece walk = told(k);
+        if (!walk.more) break;
         const int* row = p.table + (size_t)walk.r * p.table_ld;
         for (int b0 = walk.b0; b0 < walk.b1 && !stop; b0 += 32) {
           const int mine = b0 + lane < walk.b1 ? __ldg(row + b0 + lane) : -1;
@@ -171,8 +205,7 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
     if (warp == 1 || warp == 3) {
       // ------------------------------------------------------------- MMA issuers: steps of their parity
       const uint32_t w = warp >> 1;
-      if (lane == 0) {
-        Q4Walk walk(p, share, 128);
+      {
         const uint32_t tO = tmem + 384;
         const uint64_t dq = sw128_desc(smem_u32(sm + SM::Q), 16, 1024);
         const uint64_t dk = sw128_desc(smem_u32(sm + SM::K), 16, 1024);
@@ -192,30 +225,35 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
           mma_commit(&bars[T_KEMPTY + sk]);
         };
         int n0 = 0, piece = 0;
-        while (walk.next()) {
+        for (int k = 0;; ++k) {
+          const TqPiece walk = told(k);
+          if (!walk.more) break;
           if (walk.b0 == walk.b1) continue;
           const int n1 = n0 + ((walk.b1 - walk.b0 + 1) >> 1);
-          wait(T_QFULL, piece & 1);
-          for (int n = n0 + ((n0 ^ (int)w) & 1); n < n1 && n < n0 + NSB; n += 2) issue_qk(n);
-          for (int n = n0 + ((n0 ^ (int)w) & 1); n < n1 && !*abort_flag; n += 2) {
-            const int sv = n % VST, b = n % NSB;
-            // PV(n-1) complete first, so that O accumulates in step order
-            if (n > n0) wait(T_PVDONE + ((n - 1) & 1), ((n - 1) >> 1) & 1);
-            wait(T_VFULL + sv, (n / VST) & 1);
-            wait(T_PFULL + b, (n / NSB) & 1);
-            if (*abort_flag) break;
-            tc_fence_after();
+          if (lane == 0) {
+            wait(T_QFULL, piece & 1);
+            for (int n = n0 + ((n0 ^ (int)w) & 1); n < n1 && n < n0 + NSB; n += 2) issue_qk(n);
+            for (int n = n0 + ((n0 ^ (int)w) & 1); n < n1 && !*abort_flag; n += 2) {
+              const int sv = n % VST, b = n % NSB;
+              // PV(n-1) complete first, so that O accumulates in step order
+              if (n > n0) wait(T_PVDONE + ((n - 1) & 1), ((n - 1) >> 1) & 1);
+              wait(T_VFULL + sv, (n / VST) & 1);
+              wait(T_PFULL + b, (n / NSB) & 1);
+              if (*abort_flag) break;
+              tc_fence_after();
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              mma_bf16_ts(tO, tmem + b * 128 + kk * 8, dv + ((sv * SM::TILE + kk * 2048) >> 4), IDESC_PV,
-                          (n > n0 || kk > 0) ? 1u : 0u);
-            mma_commit(&bars[T_VEMPTY + sv]);
-            mma_commit(&bars[T_PVDONE + (n & 1)]);
-            if (n + NSB < n1) issue_qk(n + NSB);
+              for (int kk = 0; kk < 8; ++kk)
+                mma_bf16_ts(tO, tmem + b * 128 + kk * 8, dv + ((sv * SM::TILE + kk * 2048) >> 4), IDESC_PV,
+                            (n > n0 || kk > 0) ? 1u : 0u);
+              mma_commit(&bars[T_VEMPTY + sv]);
+              mma_commit(&bars[T_PVDONE + (n & 1)]);
+              if (n + NSB < n1) issue_qk(n + NSB);
+            }
+            // all MMAs of both issuers: the tile's O is complete, Q and the operand stages are free
+            mma_commit(&bars[T_MMADONE]);
+            mbar_wait(&bars[T_MMADONE], piece & 1, kWaitLimitNs);
           }
-          // all MMAs of both issuers: the tile's O is complete, Q and the operand stages are free
-          mma_commit(&bars[T_MMADONE]);
-          mbar_wait(&bars[T_MMADONE], piece & 1, kWaitLimitNs);
+          __syncwarp();
           n0 = n1;
           ++piece;
         }
@@ -226,9 +264,10 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
     setmaxnreg_dec<REG_UNPACK>();
     // --------------------------------------------------------------- unpack
     const int t = tid - 128, uw = warp - 4;
-    Q4Walk walk(p, share, 128);
     int n = 0, piece = 0;
-    while (walk.next()) {
+    for (int k = 0;; ++k) {
+      const TqPiece walk = told(k);
+      if (!walk.more) break;
       if (walk.b0 == walk.b1) continue;
       // Q: one row a thread, and its sum
       if (piece > 0) wait(T_MMADONE, (piece - 1) & 1);
@@ -239,16 +278,20 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
         const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
                                                           (long long)(walk.q0 + tok) * p.q_ld +
                                                           (long long)(walk.h * p.group + hd) * D);
-        float sum = 0.f;
+        float sum = 0.f, abs_sum = 0.f;
 #pragma unroll 4
         for (int c = 0; c < D / 8; ++c) {
           const uint4 v = live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
           const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sum += lo_bf16(u[i]) + hi_bf16(u[i]);
+          for (int i = 0; i < 4; ++i) {
+            sum += lo_bf16(u[i]) + hi_bf16(u[i]);
+            abs_sum += fabsf(lo_bf16(u[i])) + fabsf(hi_bf16(u[i]));
+          }
           *reinterpret_cast<uint4*>(sm + SM::Q + (c >> 3) * 16384 + t * 128 + (((c & 7) ^ (t & 7)) << 4)) = v;
         }
         reinterpret_cast<float*>(sm + SM::QS)[t] = sum;
+        reinterpret_cast<float*>(sm + SM::QS)[128 + t] = abs_sum;
         fence_proxy_async_smem();
         mbar_arrive(&bars[T_QFULL]);
       }
@@ -263,71 +306,92 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
           const float s = lo_bf16(w);
           sc[t] = s * p.scale_log2;
           sc[128 + t] = fmaf(-128.f, s, hi_bf16(w)) * p.scale_log2;
+          // a key's channels lie between m and m + 15 s
+          const float big = fmaxf(fabsf(hi_bf16(w)), fabsf(fmaf(15.f, s, hi_bf16(w)))) * p.scale_log2;
+          const bool fine = fabsf(s) < INFINITY && fabsf(hi_bf16(w)) < INFINITY;
+          const uint32_t most = __reduce_max_sync(0xffffffffu, fine ? __float_as_uint(big) : 0x7F800000u);
+          if (lane == 0) reinterpret_cast<uint32_t*>(sm + SM::KB)[(n % SCS) * 4 + uw] = most;
           if (t == 0) sc_ok[n % SCS] = (ok0 ? 1 : 0) | (ok1 ? 2 : 0);
           mbar_arrive(&bars[T_SCFULL + n % SCS]);
         }
-        wait(T_KEMPTY + sk, ((n / KST) & 1) ^ 1);
         // K: 16 (D = 64: 8) code bytes a lane; 8 lanes write 4 rows of two neighbouring column groups, 8
-        // different 16-byte columns after the swizzle
+        // different 16-byte columns after the swizzle.  All of a thread's codes are read before the first is used.
         {
           constexpr int W = Q::WORDS;                   // words of a lane's bytes; 4 lanes a row
           const int row8 = ((lane >> 4) & 1) * 4 + ((lane >> 1) & 3), j = ((lane >> 3) & 1) * 2 + (lane & 1);
-          uint8_t* dst = sm + SM::K + sk * SM::TILE;
+          const int row0 = uw * 32 + row8;              // key of the step; + 8 a turn
+          const uint8_t* src = codes + (uw >> 1) * Q::BYTES + (row0 & 63) * Q::KROW + j * Q::LANE;
+          uint32_t w[4][W];
 #pragma unroll
           for (int it = 0; it < 4; ++it) {
-            const int row = uw * 32 + it * 8 + row8;    // key of the step
-            const uint8_t* src = codes + (row >> 6) * Q::BYTES + (row & 63) * Q::KROW + j * Q::LANE;
-            uint32_t w[W];
             if (W == 4) {
-              const uint4 v = *reinterpret_cast<const uint4*>(src);
-              w[0] = v.x; w[1] = v.y; w[W - 2] = v.z; w[W - 1] = v.w;
+              const uint4 v = *reinterpret_cast<const uint4*>(src + it * 8 * Q::KROW);
+              w[it][0] = v.x; w[it][1] = v.y; w[it][W - 2] = v.z; w[it][W - 1] = v.w;
             } else {
-              const uint2 v = *reinterpret_cast<const uint2*>(src);
-              w[0] = v.x; w[1] = v.y;
+              const uint2 v = *reinterpret_cast<const uint2*>(src + it * 8 * Q::KROW);
+              w[it][0] = v.x; w[it][1] = v.y;
             }
+          }
+          uint8_t* dst = sm + SM::K + sk * SM::TILE + ((j * W) >> 3) * 16384 + row0 * 128;
+          wait(T_KEMPTY + sk, ((n / KST) & 1) ^ 1);
 #pragma unroll
-            for (int i = 0; i < W; ++i) {
-              const int c = j * W + i;                  // 16-byte column
-              *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4)) =
-                  make_uint4(nibble_pair<0>(w[i]), nibble_pair<1>(w[i]), nibble_pair<2>(w[i]), nibble_pair<3>(w[i]));
-            }
+          for (int i = 0; i < W; ++i) {
+            const int at = (((j * W + i) & 7) ^ row8) << 4;   // 16-byte column, swizzled
+#pragma unroll
+            for (int it = 0; it < 4; ++it)
+              *reinterpret_cast<uint4*>(dst + it * 1024 + at) = make_uint4(
+                  nibble_pair<0>(w[it][i]), nibble_pair<1>(w[it][i]), nibble_pair<2>(w[it][i]), nibble_pair<3>(w[it][i]));
           }
           fence_proxy_async_smem();
           mbar_arrive(&bars[T_KFULL + sk]);
         }
-        wait(T_VEMPTY + sv, ((n / VST) & 1) ^ 1);
-        // V: 8 channels of two tokens a lane
+        // V: 8 channels of two tokens a lane and turn, a block's turns together
         {
           constexpr int HALVES = D / 64;                // 8-channel halves of a lane's bytes in the layout
-          constexpr int PER = 8 * 4 * HALVES;           // tasks of 8 tokens
-          uint8_t* dst = sm + SM::V + sv * SM::TILE;
-          const int left = walk.kv_len - b * BT;        // tokens of this step that are cached
-#pragma unroll 2
-          for (int e = t; e < 16 * PER; e += 128) {
-            const int k = e % HALVES, j = (e / HALVES) & 3, g = (e / (HALVES * 4)) & 7, u8 = e / PER;
-            const int row = u8 * 8 + 2 * j;             // of the step's 128 keys
-            const uint8_t* blk = codes + (row >> 6) * Q::BYTES;
-            const uint2 w = *reinterpret_cast<const uint2*>(blk + Q::OFF_V + ((u8 & 7) * 32 + g * 4 + j) * Q::LANE + 8 * k);
-            uint2 sc = *reinterpret_cast<const uint2*>(blk + Q::OFF_VS + (row & 63) * 4);
-            const bool ok = row < 64 ? ok0 : ok1;
-            if (!ok || row >= left) sc.x = 0u;
-            if (!ok || row + 1 >= left) sc.y = 0u;
-            const uint32_t s0 = __byte_perm(sc.x, 0, 0x1010), m0 = __byte_perm(sc.x, 0, 0x3232);
-            const uint32_t s1 = __byte_perm(sc.y, 0, 0x1010), m1 = __byte_perm(sc.y, 0, 0x3232);
-            uint32_t x[8] = {nibble_pair<0>(w.x), nibble_pair<1>(w.x), nibble_pair<2>(w.x), nibble_pair<3>(w.x),
-                             nibble_pair<0>(w.y), nibble_pair<1>(w.y), nibble_pair<2>(w.y), nibble_pair<3>(w.y)};
-            uint32_t a[4], c[4];
+          constexpr int PER = 8 * 4 * HALVES;           // threads of 8 tokens
+          constexpr int GROUPS = 128 / PER, TURNS = 8 / GROUPS;
+          const int k = t % HALVES, j = (t / HALVES) & 3, g = (t / (HALVES * 4)) & 7, u8 = t / PER;
+          const int col = g * HALVES + k, row0 = u8 * 8 + 2 * j;
+          const int at0 = ((col & 7) ^ (2 * j)) << 4, at1 = 128 + (((col & 7) ^ (2 * j + 1)) << 4);
+          uint8_t* dst = sm + SM::V + sv * SM::TILE + (col >> 3) * 16384 + row0 * 128;
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            const uint8_t* blk = codes + half * Q::BYTES;
+            const uint8_t* src = blk + Q::OFF_V + (u8 * 32 + g * 4 + j) * Q::LANE + 8 * k;
+            uint2 w[TURNS], sc[TURNS];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t lo = sub_bf16x2(x[2 * i], 0x43004300u), hi = sub_bf16x2(x[2 * i + 1], 0x43004300u);
-              a[i] = fma_bf16x2(__byte_perm(lo, hi, 0x5410), s0, m0);
-              c[i] = fma_bf16x2(__byte_perm(lo, hi, 0x7632), s1, m1);
+            for (int i = 0; i < TURNS; ++i) {
+              w[i] = *reinterpret_cast<const uint2*>(src + i * GROUPS * 32 * Q::LANE);
+              sc[i] = *reinterpret_cast<const uint2*>(blk + Q::OFF_VS + (row0 + i * GROUPS * 8) * 4);
             }
-            const int col = g * HALVES + k;
-            uint8_t* at = dst + (col >> 3) * 16384;
-            *reinterpret_cast<uint4*>(at + row * 128 + (((col & 7) ^ (row & 7)) << 4)) = make_uint4(a[0], a[1], a[2], a[3]);
-            *reinterpret_cast<uint4*>(at + (row + 1) * 128 + (((col & 7) ^ ((row + 1) & 7)) << 4)) =
-                make_uint4(c[0], c[1], c[2], c[3]);
+            // tokens of this block that are cached (none of a block that is not there)
+            const int left = (half ? ok1 : ok0) ? walk.kv_len - (b + half) * BT : 0;
+            if (left < BT) {
+#pragma unroll
+              for (int i = 0; i < TURNS; ++i) {
+                if (row0 + i * GROUPS * 8 >= left) sc[i].x = 0u;
+                if (row0 + i * GROUPS * 8 + 1 >= left) sc[i].y = 0u;
+              }
+            }
+            if (half == 0) wait(T_VEMPTY + sv, ((n / VST) & 1) ^ 1);
+#pragma unroll
+            for (int i = 0; i < TURNS; ++i) {
+              const uint32_t s0 = __byte_perm(sc[i].x, 0, 0x1010), m0 = __byte_perm(sc[i].x, 0, 0x3232);
+              const uint32_t s1 = __byte_perm(sc[i].y, 0, 0x1010), m1 = __byte_perm(sc[i].y, 0, 0x3232);
+              const uint32_t y[8] = {nibble_pair<0>(w[i].x), nibble_pair<1>(w[i].x), nibble_pair<2>(w[i].x),
+                                     nibble_pair<3>(w[i].x), nibble_pair<0>(w[i].y), nibble_pair<1>(w[i].y),
+                                     nibble_pair<2>(w[i].y), nibble_pair<3>(w[i].y)};
+              uint32_t a[4], c[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const uint32_t lo = sub_bf16x2(y[2 * q], 0x43004300u), hi = sub_bf16x2(y[2 * q + 1], 0x43004300u);
+                a[q] = fma_bf16x2(__byte_perm(lo, hi, 0x5410), s0, m0);
+                c[q] = fma_bf16x2(__byte_perm(lo, hi, 0x7632), s1, m1);
+              }
+              uint8_t* to = dst + half * 8192 + i * GROUPS * 1024;
+              *reinterpret_cast<uint4*>(to + at0) = make_uint4(a[0], a[1], a[2], a[3]);
+              *reinterpret_cast<uint4*>(to + at1) = make_uint4(c[0], c[1], c[2], c[3]);
+            }
           }
           fence_proxy_async_smem();
           mbar_arrive(&bars[T_VFULL + sv]);
@@ -344,10 +408,11 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
     const int row = wq * 32 + lane;
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const uint32_t tO = tmem + lane_off + 384;
-    float2* mref = reinterpret_cast<float2*>(sm + SM::MREF);   // (reference of the next step, factor to it)
-    Q4Walk walk(p, share, 128);
+    float2* mref = reinterpret_cast<float2*>(sm + SM::MREF);   // (the last step's reference, the one it proposes)
     int n0 = 0, piece = 0;
-    while (walk.next()) {
+    for (int k = 0;; ++k) {
+      const TqPiece walk = told(k);
+      if (!walk.more) break;
       const int n1 = n0 + ((walk.b1 - walk.b0 + 1) >> 1);
       const int rr = walk.mt * 128 + row;
       const bool live = rr < walk.rows;
@@ -367,11 +432,11 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
       }
       const int lim = live && p.causal ? max(walk.kv_len - walk.q_len + rr / p.group + 1, 0) : walk.kv_len;
       wait(T_QFULL, piece & 1);
-      const float qs = reinterpret_cast<const float*>(sm + SM::QS)[row];
-      // A row has one reference for O and every l, handed from step to step with the factor that takes
-      // what was summed before to it.  l is this warpgroup's share of the row's sum, against the reference
-      // m it last used.
-      float m = -INFINITY, l = 0.f;
+      const float qs = reinterpret_cast<const float*>(sm + SM::QS)[row], qa = reinterpret_cast<const float*>(sm + SM::QS)[128 + row];
+      // A step's P is taken against a reference R that the steps before the last one left, so the two
+      // warpgroups' passes overlap; what O was summed against before (the last step's R) is read at the pass's
+      // end.  l is this warpgroup's share of the row's sum, against the reference m it last used.
+      float m = -INFINITY, l = 0.f, T = -INFINITY;   // T: reference of this warpgroup's next step
       for (int n = n0 + ((n0 ^ wg) & 1); n < n1; n += 2) {
         const int b = n % NSB;
         const uint32_t tS = tmem + lane_off + b * 128;
@@ -379,53 +444,62 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
         const float4* s4 = reinterpret_cast<const float4*>(sm + SM::SC) + (n % SCS) * 64;
         const int ok = sc_ok[n % SCS];
         wait(T_SFULL + b, (n / NSB) & 1);
+        if (n == n0 + 1) {   // the piece's first step of the other warpgroup has found a reference
+          wait(T_XDONE + (wg ^ 1), ((n - 1) >> 1) & 1);
+          T = mref[row].y;
+        }
         if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
         tc_fence_after();
-        uint32_t x[4][32];
-        tmem_ld32(tS + 0, x[0]);
-        tmem_ld32(tS + 32, x[1]);
-        tmem_ld32(tS + 64, x[2]);
-        tmem_ld32(tS + 96, x[3]);
-        tmem_wait_ld();
         const int see = lim - (walk.b0 + 2 * (n - n0)) * BT;    // of the step's keys
-        const bool cut = __any_sync(0xffffffffu, see < 128) || ok != 3;
-        // the warpgroups take turns on the exponentials; the hand-off carries the reference
-        if (n > n0) wait(T_XDONE + (wg ^ 1), ((n - 1) >> 1) & 1);
-        float R = -INFINITY, alpha = 1.f, neg, mx, ls[4];
-        if (n > n0) {
-          const float2 v = mref[row];
-          R = v.x;
-          alpha = v.y;
-        }
-        // P = 2^(x - R) over S as bf16 pairs, its row sum, and the maximum of x - R (plain: R enters the fused
-        // product, whose rounding is far below 1 then) or of x (careful: x first, so that its maximum less
-        // itself is zero however large it is; masked keys)
-        auto pass = [&](auto careful) {
-          mx = -INFINITY;
-          float mx1 = -INFINITY;
-          ls[0] = ls[1] = ls[2] = ls[3] = 0.f;
-#pragma unroll
+        const float4 kb = reinterpret_cast<const float4*>(sm + SM::KB)[n % SCS];
+        const float reach = qa * fmaxf(fmaxf(kb.x, kb.y), fmaxf(kb.z, kb.w));   // no |x| of the step is larger
+        float R = T, top = -INFINITY;
+        // P = 2^(x - R) may be as large as 2^100 or so.  Where a bound on the scores does not promise that (or no key
+        // has been seen yet), where keys are masked, and where R is so large that its rounding in the fused product
+        // would count, x is first written over S and its maximum found: R then moves up to it if need be, and the
+        // maximum less itself is zero however large it is.
+        const bool first_max = __any_sync(0xffffffffu, see < 128 || !(reach - R <= 100.f) || fabsf(R) > 4096.f) || ok != 3;
+        if (first_max) {
+#pragma unroll 1
           for (int q = 0; q < 4; ++q) {
+            uint32_t x[32];
+            tmem_ld32(tS + q * 32, x);
+            tmem_wait_ld();
+            const int to = (ok >> (q >> 1)) & 1 ? see - q * 32 : 0;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const float4 s = s4[q * 8 + e / 4], o = s4[32 + q * 8 + e / 4];
+              x[e] = __float_as_uint(to <= e ? -INFINITY : fmaf(__uint_as_float(x[e]), s.x, o.x * qs));
+              x[e + 1] = __float_as_uint(to <= e + 1 ? -INFINITY : fmaf(__uint_as_float(x[e + 1]), s.y, o.y * qs));
+              x[e + 2] = __float_as_uint(to <= e + 2 ? -INFINITY : fmaf(__uint_as_float(x[e + 2]), s.z, o.z * qs));
+              x[e + 3] = __float_as_uint(to <= e + 3 ? -INFINITY : fmaf(__uint_as_float(x[e + 3]), s.w, o.w * qs));
+              top = fmax3(top, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+              top = fmax3(top, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+            }
+            tmem_st32(tS + q * 32, x);
+          }
+          tmem_wait_st();
+          s4 = reinterpret_cast<const float4*>(sm + SM::IDENT);
+          if (R == -INFINITY || top > R + 64.f) R = top;
+        }
+        const float neg = R == -INFINITY ? 0.f : -R;
+        float mx0 = -INFINITY, mx1 = -INFINITY, ls[4] = {0.f, 0.f, 0.f, 0.f};
+        // The pass: 32 columns at a time, the next ones in flight.  P (bf16 pairs) of columns 32q .. takes columns
+        // 16q .. 16q + 15, which have been read.
+        {
+          uint32_t xa[32], xb[32];
+          auto chunk = [&](const uint32_t (&x)[32], int q) {
             uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
               const float4 s = s4[q * 8 + e / 4], o = s4[32 + q * 8 + e / 4];
               float y0, y1, y2, y3, o0, o1, o2, o3;
-              const float off = decltype(careful)::value ? 0.f : neg;
-              ffma2(o.x, o.y, qs, off, o0, o1);
-              ffma2(o.z, o.w, qs, off, o2, o3);
-              fma2(__uint_as_float(x[q][e]), __uint_as_float(x[q][e + 1]), s.x, s.y, o0, o1, y0, y1);
-              fma2(__uint_as_float(x[q][e + 2]), __uint_as_float(x[q][e + 3]), s.z, s.w, o2, o3, y2, y3);
-              if (decltype(careful)::value) {
-                const int to = (ok >> (q >> 1)) & 1 ? see - q * 32 - e : 0;
-                if (to <= 0) y0 = -INFINITY;
-                if (to <= 1) y1 = -INFINITY;
-                if (to <= 2) y2 = -INFINITY;
-                if (to <= 3) y3 = -INFINITY;
-              }
-              mx = fmax3(mx, y0, y1);
+              ffma2(o.x, o.y, qs, neg, o0, o1);
+              ffma2(o.z, o.w, qs, neg, o2, o3);
+              fma2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]), s.x, s.y, o0, o1, y0, y1);
+              fma2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]), s.z, s.w, o2, o3, y2, y3);
+              mx0 = fmax3(mx0, y0, y1);
               mx1 = fmax3(mx1, y2, y3);
-              if (decltype(careful)::value) { y0 += neg; y1 += neg; y2 += neg; y3 += neg; }
               y0 = ex2_approx(y0);
               y1 = ex2_approx(y1);
               y2 = ex2_approx(y2);
@@ -436,31 +510,50 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
               pk[e / 2 + 1] = pack_bf16(y2, y3);
             }
             tmem_st16(tS + q * 16, pk);
-          }
-          mx = fmaxf(mx, mx1);
-        };
-        // Scores may exceed the reference: P up to 2^64 fits its type, and the next step's reference follows.
-        // Above that, and where no key has been seen yet, the pass is done again against the row's maximum.
-        // (Twice at the most: a maximum found by a plain pass may be rounded, a careful one's is not.)
+          };
+          tmem_ld32(tS, xa);
 #pragma unroll 1
-        for (int turn = 0;; ++turn) {
-          neg = R == -INFINITY ? 0.f : -R;
-          const bool careful = cut || __any_sync(0xffffffffu, fabsf(neg) > 4096.f);
-          if (careful) pass(Yes{});
-          else pass(No{});
-          const float top = careful ? mx : mx - neg;       // the row's maximum of x in this step
-          if (careful) mx = mx + neg;
-          const bool again = R == -INFINITY ? top > -INFINITY : mx > 64.f;
-          if (turn == 3 || !__any_sync(0xffffffffu, again)) break;
-          if (again) {
-            if (R != -INFINITY) alpha *= ex2_approx(-mx);
-            R = top;
+          for (int q = 0; q < 4; q += 2) {
+            tmem_wait_ld();
+            tmem_ld32(tS + (q + 1) * 32, xb);
+            chunk(xa, q);
+            tmem_wait_ld();
+            if (q == 0) tmem_ld32(tS + 64, xa);
+            chunk(xb, q + 1);
           }
         }
-        {
-          const bool grow = mx > 8.f && R != -INFINITY;
-          mref[row] = grow ? make_float2(R + mx, ex2_approx(-mx)) : make_float2(R, 1.f);
+        if (!first_max) top = fmaxf(mx0, mx1) - neg;
+        // what O was summed against, and the reference that the last step proposes
+        float alpha = 1.f;
+        if (n > n0) {
+          wait(T_XDONE + (wg ^ 1), ((n - 1) >> 1) & 1);
+          const float2 v = mref[row];
+          T = v.y;
+          // O is against v.x.  Far above this step's reference (only if the last step met far larger scores), P and its
+          // sum go down to it instead of O up.
+          const bool down = v.x > R + 64.f;
+          if (__any_sync(0xffffffffu, down)) {
+            const float f = down && R != -INFINITY ? ex2_approx(R - v.x) : 1.f;
+            const uint32_t f2 = pack_bf16(f, f);
+#pragma unroll 1
+            for (int q = 0; q < 2; ++q) {
+              uint32_t pk[32];
+              tmem_wait_st();
+              tmem_ld32(tS + q * 32, pk);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(pk[e]) : "r"(pk[e]), "r"(f2));
+              tmem_st32(tS + q * 32, pk);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ls[i] *= f;
+            if (down) R = v.x;
+          }
+          alpha = v.x == R || v.x == -INFINITY ? 1.f : ex2_approx(v.x - R);
         }
+        T = fmaxf(T, top > R + 8.f ? top : R);
+        mref[row] = make_float2(R, T);
         mbar_arrive(&bars[T_XDONE + wg]);
         if (m != -INFINITY && m != R) l *= ex2_approx(m - R);
         m = R;
@@ -518,7 +611,6 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
       n0 = n1;
       ++piece;
     }
-    if (tid == 256) p.desc[blockIdx.x] = walk.desc;
   }
 
   // ----------------------------------------------------------------- teardown
