@@ -12,13 +12,12 @@
 //    pbsa_expand_q4 gives.  The scores then get their scale and minimum in fp32, per key:
 //      x = s (q . (c + 128)) + (m - 128 s) sum(q),
 //    so they carry no rounding of K; rounding K to bf16 would put 2^-8 |q . k| / sqrt(d) of noise into each.
-//  * TMEM: three S/P buffers and one O accumulator (512 columns), two softmax warpgroups on alternate
-//    steps, two MMA-issuing threads, P over S as bf16.  S(i+3) is issued behind PV(i), so a warpgroup never
-//    waits for its own PV.  The softmax makes one pass over a step's scores: scale, exponential, sum and
-//    maximum together, against the reference that the steps before the last one left, so the two warpgroups'
-//    passes overlap.  A step whose maximum exceeds it by 2^8 moves the reference for a later one (O is
-//    rescaled then).  P of the step itself may be as large as 2^100; where a bound on its scores does not
-//    promise that, their maximum is found first.
+//  * TMEM: two S, two P (bf16) and one O (512 columns at D = 128); two softmax warpgroups on alternate steps, two
+//    MMA-issuing threads, one for each.  QK(i+2) is issued as soon as S(i) has been read, ahead of PV(i).
+//    The softmax makes one pass over a step's scores: scale, exponential, sum and maximum together, against
+//    the reference that the steps before the last one left, so the two warpgroups' passes overlap.  A step
+//    whose maximum exceeds it by 2^8 moves the reference for a later one (O is rescaled then); P of the step
+//    itself may be as large as 2^64, above which the pass is done again from S.
 //  * All barriers are used once per step with a step count that runs on over the pieces (a piece without
 //    blocks takes part in none).  The ring of key scales has four places: the unpackers reach step n only when
 //    PV(n-3), and so the softmax of step n-3, is done.
@@ -35,13 +34,13 @@ namespace {
 
 constexpr int TQ_THREADS = 512;      // warpgroups: control, unpack, softmax x 2
 constexpr int TQ_MIN_STEPS = 8;      // blocks that are worth a CTA of their own
-constexpr int CST = 3, KST = 2, VST = 2, NSB = 3, SCS = 4;
+constexpr int CST = 3, KST = 2, VST = 2, SCS = 4;
 constexpr uint32_t REG_CTRL = 48, REG_UNPACK = 80, REG_SOFT = 192;   // launched with 128: 48 + 80 + 2*192 = 4*128
 static_assert(REG_CTRL + REG_UNPACK + 2 * REG_SOFT <= 4 * 128, "register split exceeds the launch");
 
 enum { T_QFULL = 0, T_CFULL = 1, T_CEMPTY = T_CFULL + CST, T_KFULL = T_CEMPTY + CST, T_KEMPTY = T_KFULL + KST,
        T_VFULL = T_KEMPTY + KST, T_VEMPTY = T_VFULL + VST, T_SCFULL = T_VEMPTY + VST, T_SFULL = T_SCFULL + SCS,
-       T_PFULL = T_SFULL + NSB, T_PVDONE = T_PFULL + NSB, T_MMADONE = T_PVDONE + 2, T_XDONE = T_MMADONE + 1,
+       T_PFULL = T_SFULL + 2, T_PVDONE = T_PFULL + 2, T_MMADONE = T_PVDONE + 2, T_XDONE = T_MMADONE + 1,
        T_WFULL = T_XDONE + 2, T_WEMPTY = T_WFULL + 2, T_BARS = T_WEMPTY + 2 };
 constexpr int WARPS_TOLD = 15;       // warps that read the pieces: all but the one that walks them
 
@@ -60,9 +59,8 @@ struct TqSmem {
   static constexpr uint32_t V = K + KST * TILE;
   static constexpr uint32_t CODES = V + VST * TILE;
   static constexpr uint32_t SC = CODES + CST * STEP;                // float [SCS][2][128]: per key, scale and offset
-  static constexpr uint32_t KB = SC + SCS * 1024;                   // float [SCS][4]: the largest |key channel| of 32 keys
-  static constexpr uint32_t QS = KB + SCS * 16;                     // float [2][128]: sums of the rows of Q, of |Q|
-  static constexpr uint32_t MREF = QS + 1024;                       // float2 [128]
+  static constexpr uint32_t QS = SC + SCS * 1024;                   // float [128]: sums of the rows of Q
+  static constexpr uint32_t MREF = QS + 512;                        // float2 [128]
   static constexpr uint32_t RLAST = MREF + 1024;                    // float [128]
   static constexpr uint32_t STAT = RLAST + 512;                     // float2 [2][128]
   static constexpr uint32_t IDENT = STAT + 2048;                    // float [2][128]: a scale of 1, an offset of 0
@@ -74,11 +72,26 @@ struct TqSmem {
 };
 static_assert(TqSmem<128>::BYTES <= 232448, "shared memory");
 
-__device__ __forceinline__ void fma2(float x0, float x1, float y0, float y1, float z0, float z1, float& d0, float& d1) {
-  asm("{\n\t.reg .b64 x, y, z, d;\n\t"
-      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-      "fma.rn.f32x2 d, x, y, z;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d0), "=f"(d1) : "f"(x0), "f"(x1), "f"(y0), "f"(y1), "f"(z0), "f"(z1));
+// Pairs of fp32 in 64-bit registers (packed f32x2 arithmetic), kept packed so that no moves pair them up.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(uint32_t lo, uint32_t hi) {
+  f32x2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+  return d;
+}
+__device__ __forceinline__ f32x2 pair(float lo, float hi) { return pair(__float_as_uint(lo), __float_as_uint(hi)); }
+__device__ __forceinline__ void parts(f32x2 d, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(d));
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 x, f32x2 y, f32x2 z) {
+  f32x2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
+  return d;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 x, f32x2 y) {
+  f32x2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+  return d;
 }
 __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -212,16 +225,16 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
         const uint64_t dv = sw128_desc(smem_u32(sm + SM::V), 16384, 1024);
         constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, 128, 0, 0), IDESC_PV = idesc_bf16_f32(128, D, 0, 1);
         auto issue_qk = [&](int n) {
-          const int sk = n % KST, b = n % NSB;
+          const int sk = n % KST;
           wait(T_KFULL + sk, (n / KST) & 1);
           if (*abort_flag) return;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-            mma_bf16_ss(tmem + b * 128, dq + off, dk + ((sk * SM::TILE) >> 4) + off, IDESC_QK, kk > 0 ? 1u : 0u);
+            mma_bf16_ss(tmem + w * 128, dq + off, dk + ((sk * SM::TILE) >> 4) + off, IDESC_QK, kk > 0 ? 1u : 0u);
           }
-          mma_commit(&bars[T_SFULL + b]);
+          mma_commit(&bars[T_SFULL + w]);
           mma_commit(&bars[T_KEMPTY + sk]);
         };
         int n0 = 0, piece = 0;
@@ -232,22 +245,23 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
           const int n1 = n0 + ((walk.b1 - walk.b0 + 1) >> 1);
           if (lane == 0) {
             wait(T_QFULL, piece & 1);
-            for (int n = n0 + ((n0 ^ (int)w) & 1); n < n1 && n < n0 + NSB; n += 2) issue_qk(n);
-            for (int n = n0 + ((n0 ^ (int)w) & 1); n < n1 && !*abort_flag; n += 2) {
-              const int sv = n % VST, b = n % NSB;
+            const int first = n0 + ((n0 ^ (int)w) & 1);
+            if (first < n1) issue_qk(first);
+            for (int n = first; n < n1 && !*abort_flag; n += 2) {
+              const int sv = n % VST;
+              wait(T_PFULL + w, (n >> 1) & 1);           // S(n) has been read, P(n) written
+              if (n + 2 < n1) issue_qk(n + 2);
               // PV(n-1) complete first, so that O accumulates in step order
-              if (n > n0) wait(T_PVDONE + ((n - 1) & 1), ((n - 1) >> 1) & 1);
+              if (n > n0) wait(T_PVDONE + (w ^ 1), ((n - 1) >> 1) & 1);
               wait(T_VFULL + sv, (n / VST) & 1);
-              wait(T_PFULL + b, (n / NSB) & 1);
               if (*abort_flag) break;
               tc_fence_after();
 #pragma unroll
               for (int kk = 0; kk < 8; ++kk)
-                mma_bf16_ts(tO, tmem + b * 128 + kk * 8, dv + ((sv * SM::TILE + kk * 2048) >> 4), IDESC_PV,
+                mma_bf16_ts(tO, tmem + 256 + w * 64 + kk * 8, dv + ((sv * SM::TILE + kk * 2048) >> 4), IDESC_PV,
                             (n > n0 || kk > 0) ? 1u : 0u);
               mma_commit(&bars[T_VEMPTY + sv]);
-              mma_commit(&bars[T_PVDONE + (n & 1)]);
-              if (n + NSB < n1) issue_qk(n + NSB);
+              mma_commit(&bars[T_PVDONE + w]);
             }
             // all MMAs of both issuers: the tile's O is complete, Q and the operand stages are free
             mma_commit(&bars[T_MMADONE]);
@@ -278,20 +292,16 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
         const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
                                                           (long long)(walk.q0 + tok) * p.q_ld +
                                                           (long long)(walk.h * p.group + hd) * D);
-        float sum = 0.f, abs_sum = 0.f;
+        float sum = 0.f;
 #pragma unroll 4
         for (int c = 0; c < D / 8; ++c) {
           const uint4 v = live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
           const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            sum += lo_bf16(u[i]) + hi_bf16(u[i]);
-            abs_sum += fabsf(lo_bf16(u[i])) + fabsf(hi_bf16(u[i]));
-          }
+          for (int i = 0; i < 4; ++i) sum += lo_bf16(u[i]) + hi_bf16(u[i]);
           *reinterpret_cast<uint4*>(sm + SM::Q + (c >> 3) * 16384 + t * 128 + (((c & 7) ^ (t & 7)) << 4)) = v;
         }
         reinterpret_cast<float*>(sm + SM::QS)[t] = sum;
-        reinterpret_cast<float*>(sm + SM::QS)[128 + t] = abs_sum;
         fence_proxy_async_smem();
         mbar_arrive(&bars[T_QFULL]);
       }
@@ -306,11 +316,6 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
           const float s = lo_bf16(w);
           sc[t] = s * p.scale_log2;
           sc[128 + t] = fmaf(-128.f, s, hi_bf16(w)) * p.scale_log2;
-          // a key's channels lie between m and m + 15 s
-          const float big = fmaxf(fabsf(hi_bf16(w)), fabsf(fmaf(15.f, s, hi_bf16(w)))) * p.scale_log2;
-          const bool fine = fabsf(s) < INFINITY && fabsf(hi_bf16(w)) < INFINITY;
-          const uint32_t most = __reduce_max_sync(0xffffffffu, fine ? __float_as_uint(big) : 0x7F800000u);
-          if (lane == 0) reinterpret_cast<uint32_t*>(sm + SM::KB)[(n % SCS) * 4 + uw] = most;
           if (t == 0) sc_ok[n % SCS] = (ok0 ? 1 : 0) | (ok1 ? 2 : 0);
           mbar_arrive(&bars[T_SCFULL + n % SCS]);
         }
@@ -432,18 +437,17 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
       }
       const int lim = live && p.causal ? max(walk.kv_len - walk.q_len + rr / p.group + 1, 0) : walk.kv_len;
       wait(T_QFULL, piece & 1);
-      const float qs = reinterpret_cast<const float*>(sm + SM::QS)[row], qa = reinterpret_cast<const float*>(sm + SM::QS)[128 + row];
+      const float qs = reinterpret_cast<const float*>(sm + SM::QS)[row];
       // A step's P is taken against a reference R that the steps before the last one left, so the two
       // warpgroups' passes overlap; what O was summed against before (the last step's R) is read at the pass's
       // end.  l is this warpgroup's share of the row's sum, against the reference m it last used.
       float m = -INFINITY, l = 0.f, T = -INFINITY;   // T: reference of this warpgroup's next step
       for (int n = n0 + ((n0 ^ wg) & 1); n < n1; n += 2) {
-        const int b = n % NSB;
-        const uint32_t tS = tmem + lane_off + b * 128;
+        const uint32_t tS = tmem + lane_off + wg * 128, tP = tmem + lane_off + 256 + wg * 64;
         wait(T_SCFULL + n % SCS, (n / SCS) & 1);
         const float4* s4 = reinterpret_cast<const float4*>(sm + SM::SC) + (n % SCS) * 64;
         const int ok = sc_ok[n % SCS];
-        wait(T_SFULL + b, (n / NSB) & 1);
+        wait(T_SFULL + wg, (n >> 1) & 1);
         if (n == n0 + 1) {   // the piece's first step of the other warpgroup has found a reference
           wait(T_XDONE + (wg ^ 1), ((n - 1) >> 1) & 1);
           T = mref[row].y;
@@ -451,69 +455,71 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
         if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
         tc_fence_after();
         const int see = lim - (walk.b0 + 2 * (n - n0)) * BT;    // of the step's keys
-        const float4 kb = reinterpret_cast<const float4*>(sm + SM::KB)[n % SCS];
-        const float reach = qa * fmaxf(fmaxf(kb.x, kb.y), fmaxf(kb.z, kb.w));   // no |x| of the step is larger
-        float R = T, top = -INFINITY;
-        // P = 2^(x - R) may be as large as 2^100 or so.  Where a bound on the scores does not promise that (or no key
-        // has been seen yet), where keys are masked, and where R is so large that its rounding in the fused product
-        // would count, x is first written over S and its maximum found: R then moves up to it if need be, and the
-        // maximum less itself is zero however large it is.
-        const bool first_max = __any_sync(0xffffffffu, see < 128 || !(reach - R <= 100.f) || fabsf(R) > 4096.f) || ok != 3;
-        if (first_max) {
+        if (n - 2 >= n0) wait(T_PVDONE + wg, ((n - 2) >> 1) & 1);   // P(n-2), in the same columns, has been used
+        float R = T, alpha = 1.f, top = -INFINITY, psum;
+        // Plain: one pass over S.  Careful, where keys are masked, where no key has been seen yet, where R is so
+        // large that its rounding in the fused product would count, and where a plain pass has met scores above
+        // R + 64 (P could pass its range): x is first written over S and its maximum found, R moves up to it if
+        // need be, and the maximum less itself is zero however large it is.
+        bool careful = __any_sync(0xffffffffu, see < 128 || R == -INFINITY || fabsf(R) > 4096.f) || ok != 3;
+        bool plain = true, joined = n == n0;
 #pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            uint32_t x[32];
-            tmem_ld32(tS + q * 32, x);
-            tmem_wait_ld();
-            const int to = (ok >> (q >> 1)) & 1 ? see - q * 32 : 0;
+        while (true) {
+          if (careful && plain) {
+            plain = false;
+            top = -INFINITY;
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+              uint32_t x[32];
+              tmem_ld32(tS + q * 32, x);
+              tmem_wait_ld();
+              const int to = (ok >> (q >> 1)) & 1 ? see - q * 32 : 0;
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 s = s4[q * 8 + e / 4], o = s4[32 + q * 8 + e / 4];
-              x[e] = __float_as_uint(to <= e ? -INFINITY : fmaf(__uint_as_float(x[e]), s.x, o.x * qs));
-              x[e + 1] = __float_as_uint(to <= e + 1 ? -INFINITY : fmaf(__uint_as_float(x[e + 1]), s.y, o.y * qs));
-              x[e + 2] = __float_as_uint(to <= e + 2 ? -INFINITY : fmaf(__uint_as_float(x[e + 2]), s.z, o.z * qs));
-              x[e + 3] = __float_as_uint(to <= e + 3 ? -INFINITY : fmaf(__uint_as_float(x[e + 3]), s.w, o.w * qs));
-              top = fmax3(top, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-              top = fmax3(top, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+              for (int e = 0; e < 32; e += 4) {
+                const float4 s = s4[q * 8 + e / 4], o = s4[32 + q * 8 + e / 4];
+                x[e] = __float_as_uint(to <= e ? -INFINITY : fmaf(__uint_as_float(x[e]), s.x, o.x * qs));
+                x[e + 1] = __float_as_uint(to <= e + 1 ? -INFINITY : fmaf(__uint_as_float(x[e + 1]), s.y, o.y * qs));
+                x[e + 2] = __float_as_uint(to <= e + 2 ? -INFINITY : fmaf(__uint_as_float(x[e + 2]), s.z, o.z * qs));
+                x[e + 3] = __float_as_uint(to <= e + 3 ? -INFINITY : fmaf(__uint_as_float(x[e + 3]), s.w, o.w * qs));
+                top = fmax3(top, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                top = fmax3(top, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+              }
+              tmem_st32(tS + q * 32, x);
             }
-            tmem_st32(tS + q * 32, x);
+            tmem_wait_st();
+            s4 = reinterpret_cast<const float4*>(sm + SM::IDENT);
+            if (R == -INFINITY || top > R + 64.f) R = top;
           }
-          tmem_wait_st();
-          s4 = reinterpret_cast<const float4*>(sm + SM::IDENT);
-          if (R == -INFINITY || top > R + 64.f) R = top;
-        }
-        const float neg = R == -INFINITY ? 0.f : -R;
-        float mx0 = -INFINITY, mx1 = -INFINITY, ls[4] = {0.f, 0.f, 0.f, 0.f};
-        // The pass: 32 columns at a time, the next ones in flight.  P (bf16 pairs) of columns 32q .. takes columns
-        // 16q .. 16q + 15, which have been read.
-        {
+          const float neg = R == -INFINITY ? 0.f : -R;
+          const f32x2 qs2 = pair(qs, qs), neg2 = pair(neg, neg);
+          float mx0 = -INFINITY, mx1 = -INFINITY;
+          f32x2 sum0 = 0ull, sum1 = 0ull;
           uint32_t xa[32], xb[32];
-          auto chunk = [&](const uint32_t (&x)[32], int q) {
+          auto chunk = [&](const uint32_t (&x)[32], int q) {   // P (bf16 pairs) of 32 columns
             uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
-              const float4 s = s4[q * 8 + e / 4], o = s4[32 + q * 8 + e / 4];
-              float y0, y1, y2, y3, o0, o1, o2, o3;
-              ffma2(o.x, o.y, qs, neg, o0, o1);
-              ffma2(o.z, o.w, qs, neg, o2, o3);
-              fma2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]), s.x, s.y, o0, o1, y0, y1);
-              fma2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]), s.z, s.w, o2, o3, y2, y3);
+              const ulonglong2 s = reinterpret_cast<const ulonglong2*>(s4)[q * 8 + e / 4];
+              const ulonglong2 o = reinterpret_cast<const ulonglong2*>(s4)[32 + q * 8 + e / 4];
+              float y0, y1, y2, y3;
+              parts(fma2(pair(x[e], x[e + 1]), s.x, fma2(o.x, qs2, neg2)), y0, y1);
+              parts(fma2(pair(x[e + 2], x[e + 3]), s.y, fma2(o.y, qs2, neg2)), y2, y3);
               mx0 = fmax3(mx0, y0, y1);
               mx1 = fmax3(mx1, y2, y3);
               y0 = ex2_approx(y0);
               y1 = ex2_approx(y1);
               y2 = ex2_approx(y2);
               y3 = ex2_approx(y3);
-              fadd2(ls[0], ls[1], y0, y1);
-              fadd2(ls[2], ls[3], y2, y3);
+              sum0 = add2(sum0, pair(y0, y1));
+              sum1 = add2(sum1, pair(y2, y3));
               pk[e / 2] = pack_bf16(y0, y1);
               pk[e / 2 + 1] = pack_bf16(y2, y3);
             }
-            tmem_st16(tS + q * 16, pk);
+            tmem_st16(tP + q * 16, pk);
           };
           tmem_ld32(tS, xa);
 #pragma unroll 1
-          for (int q = 0; q < 4; q += 2) {
+          for (int q = 0; q < 4; q += 2) {                     // the next columns in flight
             tmem_wait_ld();
             tmem_ld32(tS + (q + 1) * 32, xb);
             chunk(xa, q);
@@ -521,43 +527,38 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
             if (q == 0) tmem_ld32(tS + 64, xa);
             chunk(xb, q + 1);
           }
-        }
-        if (!first_max) top = fmaxf(mx0, mx1) - neg;
-        // what O was summed against, and the reference that the last step proposes
-        float alpha = 1.f;
-        if (n > n0) {
+          {
+            float a, b;
+            parts(add2(sum0, sum1), a, b);
+            psum = a + b;
+          }
+          if (plain) {
+            const float mx = fmaxf(mx0, mx1);
+            top = mx - neg;
+            if (__any_sync(0xffffffffu, mx > 64.f)) {
+              careful = true;
+              continue;
+            }
+          }
+          if (joined) break;
+          // What O was summed against (v.x), and the reference that the last step proposes.  If that step met far
+          // larger scores, this step's P is taken against its reference instead.
+          joined = true;
           wait(T_XDONE + (wg ^ 1), ((n - 1) >> 1) & 1);
           const float2 v = mref[row];
           T = v.y;
-          // O is against v.x.  Far above this step's reference (only if the last step met far larger scores), P and its
-          // sum go down to it instead of O up.
-          const bool down = v.x > R + 64.f;
-          if (__any_sync(0xffffffffu, down)) {
-            const float f = down && R != -INFINITY ? ex2_approx(R - v.x) : 1.f;
-            const uint32_t f2 = pack_bf16(f, f);
-#pragma unroll 1
-            for (int q = 0; q < 2; ++q) {
-              uint32_t pk[32];
-              tmem_wait_st();
-              tmem_ld32(tS + q * 32, pk);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(pk[e]) : "r"(pk[e]), "r"(f2));
-              tmem_st32(tS + q * 32, pk);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) ls[i] *= f;
-            if (down) R = v.x;
-          }
-          alpha = v.x == R || v.x == -INFINITY ? 1.f : ex2_approx(v.x - R);
+          alpha = v.x;
+          const bool again = v.x > R + 64.f && R != -INFINITY;
+          if (again || R == -INFINITY) R = v.x;
+          if (!__any_sync(0xffffffffu, again)) break;
         }
+        if (n > n0) alpha = alpha == R || alpha == -INFINITY ? 1.f : ex2_approx(alpha - R);
         T = fmaxf(T, top > R + 8.f ? top : R);
         mref[row] = make_float2(R, T);
         mbar_arrive(&bars[T_XDONE + wg]);
         if (m != -INFINITY && m != R) l *= ex2_approx(m - R);
         m = R;
-        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        l += psum;
         if (n > n0 && __any_sync(0xffffffffu, alpha != 1.f)) {     // tcgen05.ld/st are warp-collective
           wait(T_PVDONE + ((n - 1) & 1), ((n - 1) >> 1) & 1);
           tc_fence_after();
@@ -573,7 +574,7 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
         }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&bars[T_PFULL + b]);
+        mbar_arrive(&bars[T_PFULL + wg]);
         if (n + 1 == n1) reinterpret_cast<float*>(sm + SM::RLAST)[row] = R;   // what O is against
       }
       // ------------------------------------------------------------- the piece's end
