@@ -7,7 +7,7 @@
 //  * Work: the line of attend_q4.cuh, with tiles of 128 rows; one CTA per SM, pieces one after another.
 //    With the causal rule a tile is charged what it sees, so long prompts are spread evenly.
 //  * Each step covers two blocks (128 keys).  Warp 0 brings the slots' bytes into a ring with bulk copies;
-//    a warpgroup of 4 warps unpacks them into shared-memory operand tiles (128-byte swizzle): K as
+//    two warpgroups, alternate steps, unpack them into shared-memory operand tiles (128-byte swizzle): K as
 //    the codes themselves (plus 128, exact in bf16), V as bf16 values s*c + m, rounded once, the bits that
 //    pbsa_expand_q4 gives.  The scores then get their scale and minimum in fp32, per key:
 //      x = s (q . (c + 128)) + (m - 128 s) sum(q),
@@ -32,17 +32,17 @@
 namespace pbsa {
 namespace {
 
-constexpr int TQ_THREADS = 512;      // warpgroups: control, unpack, softmax x 2
+constexpr int TQ_THREADS = 640;      // warpgroups: control, unpack x 2, softmax x 2
 constexpr int TQ_MIN_STEPS = 8;      // blocks that are worth a CTA of their own
 constexpr int CST = 3, KST = 2, VST = 2, SCS = 4;
-constexpr uint32_t REG_CTRL = 48, REG_UNPACK = 80, REG_SOFT = 192;   // launched with 128: 48 + 80 + 2*192 = 4*128
-static_assert(REG_CTRL + REG_UNPACK + 2 * REG_SOFT <= 4 * 128, "register split exceeds the launch");
+constexpr uint32_t REG_CTRL = 48, REG_UNPACK = 80, REG_SOFT = 136;   // launched with 96: 48 + 2*80 + 2*136 = 5*96
+static_assert(REG_CTRL + 2 * REG_UNPACK + 2 * REG_SOFT <= 5 * 96, "register split exceeds the launch");
 
 enum { T_QFULL = 0, T_CFULL = 1, T_CEMPTY = T_CFULL + CST, T_KFULL = T_CEMPTY + CST, T_KEMPTY = T_KFULL + KST,
        T_VFULL = T_KEMPTY + KST, T_VEMPTY = T_VFULL + VST, T_SCFULL = T_VEMPTY + VST, T_SFULL = T_SCFULL + SCS,
        T_PFULL = T_SFULL + 2, T_PVDONE = T_PFULL + 2, T_MMADONE = T_PVDONE + 2, T_XDONE = T_MMADONE + 1,
        T_WFULL = T_XDONE + 2, T_WEMPTY = T_WFULL + 2, T_BARS = T_WEMPTY + 2 };
-constexpr int WARPS_TOLD = 15;       // warps that read the pieces: all but the one that walks them
+constexpr int WARPS_TOLD = 19;       // warps that read the pieces: all but the one that walks them
 
 // A piece of the CTA's share, as the walking warp passes it on.
 struct TqPiece {
@@ -59,8 +59,8 @@ struct TqSmem {
   static constexpr uint32_t V = K + KST * TILE;
   static constexpr uint32_t CODES = V + VST * TILE;
   static constexpr uint32_t SC = CODES + CST * STEP;                // float [SCS][2][128]: per key, scale and offset
-  static constexpr uint32_t QS = SC + SCS * 1024;                   // float [128]: sums of the rows of Q
-  static constexpr uint32_t MREF = QS + 512;                        // float2 [128]
+  static constexpr uint32_t QS = SC + SCS * 1024;                   // float [2][128]: sums of the halves of Q's rows
+  static constexpr uint32_t MREF = QS + 1024;                       // float2 [128]
   static constexpr uint32_t RLAST = MREF + 1024;                    // float [128]
   static constexpr uint32_t STAT = RLAST + 512;                     // float2 [2][128]
   static constexpr uint32_t IDENT = STAT + 2048;                    // float [2][128]: a scale of 1, an offset of 0
@@ -120,9 +120,9 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
 
   if (tid == 0) {
     for (int i = 0; i < T_BARS; ++i) {
-      const bool many = i == T_QFULL || (i >= T_CEMPTY && i < T_KEMPTY) || (i >= T_VFULL && i < T_VEMPTY) ||
+      const bool many = (i >= T_CEMPTY && i < T_KEMPTY) || (i >= T_VFULL && i < T_VEMPTY) ||
                         (i >= T_SCFULL && i < T_SFULL) || (i >= T_PFULL && i < T_PVDONE) || (i >= T_XDONE && i < T_WFULL);
-      mbar_init(&bars[i], many ? 128 : i == T_MMADONE ? 2 : i >= T_WEMPTY ? WARPS_TOLD : 1);
+      mbar_init(&bars[i], many ? 128 : i == T_QFULL ? 256 : i == T_MMADONE ? 2 : i >= T_WEMPTY ? WARPS_TOLD : 1);
     }
     *abort_flag = 0;
     fence_barrier_init();
@@ -274,16 +274,16 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
       }
       __syncwarp();
     }
-  } else if (warp < 8) {
+  } else if (warp < 12) {
     setmaxnreg_dec<REG_UNPACK>();
-    // --------------------------------------------------------------- unpack
-    const int t = tid - 128, uw = warp - 4;
+    // --------------------------------------------------------------- unpack: steps of the warpgroup's parity
+    const int ug = (warp - 4) >> 2, t = tid & 127, uw = warp & 3;
     int n = 0, piece = 0;
     for (int k = 0;; ++k) {
       const TqPiece walk = told(k);
       if (!walk.more) break;
       if (walk.b0 == walk.b1) continue;
-      // Q: one row a thread, and its sum
+      // Q: half a row a thread, and its sum
       if (piece > 0) wait(T_MMADONE, (piece - 1) & 1);
       {
         const int rr = walk.mt * 128 + t;
@@ -294,18 +294,20 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
                                                           (long long)(walk.h * p.group + hd) * D);
         float sum = 0.f;
 #pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
+        for (int c = ug * (D / 16); c < (ug + 1) * (D / 16); ++c) {
           const uint4 v = live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
           const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) sum += lo_bf16(u[i]) + hi_bf16(u[i]);
           *reinterpret_cast<uint4*>(sm + SM::Q + (c >> 3) * 16384 + t * 128 + (((c & 7) ^ (t & 7)) << 4)) = v;
         }
-        reinterpret_cast<float*>(sm + SM::QS)[t] = sum;
+        reinterpret_cast<float*>(sm + SM::QS)[ug * 128 + t] = sum;
         fence_proxy_async_smem();
         mbar_arrive(&bars[T_QFULL]);
       }
-      for (int b = walk.b0; b < walk.b1; b += 2, ++n) {
+      const int n1 = n + ((walk.b1 - walk.b0 + 1) >> 1), first = n;
+      for (n += (n ^ ug) & 1; n < n1; n += 2) {
+        const int b = walk.b0 + 2 * (n - first);
         const int cs = n % CST, sk = n % KST, sv = n % VST;
         wait(T_CFULL + cs, (n / CST) & 1);
         const uint8_t* codes = sm + SM::CODES + cs * SM::STEP;
@@ -403,12 +405,13 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
         }
         mbar_arrive(&bars[T_CEMPTY + cs]);
       }
+      n = n1;
       ++piece;
     }
   } else {
     setmaxnreg_inc<REG_SOFT>();
     // --------------------------------------------------------------- softmax
-    const int wg = (warp - 8) >> 2;          // steps of this parity
+    const int wg = (warp - 12) >> 2;         // steps of this parity
     const int wq = warp & 3;                 // TMEM lane quadrant this warp may access
     const int row = wq * 32 + lane;
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
@@ -437,7 +440,7 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
       }
       const int lim = live && p.causal ? max(walk.kv_len - walk.q_len + rr / p.group + 1, 0) : walk.kv_len;
       wait(T_QFULL, piece & 1);
-      const float qs = reinterpret_cast<const float*>(sm + SM::QS)[row];
+      const float qs = reinterpret_cast<const float*>(sm + SM::QS)[row] + reinterpret_cast<const float*>(sm + SM::QS)[128 + row];
       // A step's P is taken against a reference R that the steps before the last one left, so the two
       // warpgroups' passes overlap; what O was summed against before (the last step's R) is read at the pass's
       // end.  l is this warpgroup's share of the row's sum, against the reference m it last used.
