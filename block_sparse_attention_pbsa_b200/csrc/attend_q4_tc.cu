@@ -19,8 +19,10 @@
 //    whose maximum exceeds it by 2^8 moves the reference for a later one (O is rescaled then); P of the step
 //    itself may be as large as 2^64, above which the pass is done again from S.
 //  * All barriers are used once per step with a step count that runs on over the pieces (a piece without
-//    blocks takes part in none).  The ring of key scales has four places: the unpackers reach step n only when
-//    PV(n-3), and so the softmax of step n-3, is done.
+//    blocks takes part in none).  The ring of key scales has four places: step n's are
+//    written once QK(n-2) is done, which follows the softmax of step n-4.
+//  * The codes of K and of V have a ring each, so that a step's K can be unpacked before the V of the step
+//    two earlier, which may have to wait for its place.
 //  * Keys that a row does not see get x = -inf by a select after the scale is applied, and V of tokens
 //    that are not cached is zero, so whatever bytes lie there reach no row.
 // Waits are bounded; on expiry the error is recorded and every role runs through its pieces without
@@ -38,7 +40,8 @@ constexpr int CST = 3, KST = 2, VST = 2, SCS = 4;
 constexpr uint32_t REG_CTRL = 48, REG_UNPACK = 80, REG_SOFT = 136;   // launched with 96: 48 + 2*80 + 2*136 = 5*96
 static_assert(REG_CTRL + 2 * REG_UNPACK + 2 * REG_SOFT <= 5 * 96, "register split exceeds the launch");
 
-enum { T_QFULL = 0, T_CFULL = 1, T_CEMPTY = T_CFULL + CST, T_KFULL = T_CEMPTY + CST, T_KEMPTY = T_KFULL + KST,
+enum { T_QFULL = 0, T_CFULL = 1, T_CEMPTY = T_CFULL + 2 * CST, T_KFULL = T_CEMPTY + 2 * CST,   // codes: K ring, V ring
+       T_KEMPTY = T_KFULL + KST,
        T_VFULL = T_KEMPTY + KST, T_VEMPTY = T_VFULL + VST, T_SCFULL = T_VEMPTY + VST, T_SFULL = T_SCFULL + SCS,
        T_PFULL = T_SFULL + 2, T_PVDONE = T_PFULL + 2, T_MMADONE = T_PVDONE + 2, T_XDONE = T_MMADONE + 1,
        T_WFULL = T_XDONE + 2, T_WEMPTY = T_WFULL + 2, T_BARS = T_WEMPTY + 2 };
@@ -53,12 +56,13 @@ template <int D>
 struct TqSmem {
   static constexpr uint32_t PANELS = D / 64;
   static constexpr uint32_t TILE = PANELS * 16384;                  // 128 rows of 64 columns a panel
-  static constexpr uint32_t STEP = 2 * Q4<D>::BYTES;
+  static constexpr uint32_t STEP = 2 * Q4<D>::HALF;                 // two blocks' K codes, or V codes
   static constexpr uint32_t Q = 0;
   static constexpr uint32_t K = TILE;
   static constexpr uint32_t V = K + KST * TILE;
   static constexpr uint32_t CODES = V + VST * TILE;
-  static constexpr uint32_t SC = CODES + CST * STEP;                // float [SCS][2][128]: per key, scale and offset
+  static constexpr uint32_t SC = CODES + 2 * CST * STEP;            // (the ring of K codes, then that of V codes;) float
+                                                                    // [SCS][2][128]: per key, scale and offset
   static constexpr uint32_t QS = SC + SCS * 1024;                   // float [2][128]: sums of the halves of Q's rows
   static constexpr uint32_t MREF = QS + 1024;                       // float2 [128]
   static constexpr uint32_t RLAST = MREF + 1024;                    // float [128]
@@ -66,8 +70,8 @@ struct TqSmem {
   static constexpr uint32_t IDENT = STAT + 2048;                    // float [2][128]: a scale of 1, an offset of 0
   static constexpr uint32_t BARS = IDENT + 1024;
   static constexpr uint32_t WALK = BARS + T_BARS * 8;               // TqPiece [2]
-  static constexpr uint32_t META = WALK + 2 * sizeof(TqPiece);      // int [CST][2], int [SCS], TMEM address, abort flag
-  static constexpr uint32_t TOTAL = META + 4 * (2 * CST + SCS + 2);
+  static constexpr uint32_t META = WALK + 2 * sizeof(TqPiece);      // int [2 CST][2], int [SCS], TMEM address, abort flag
+  static constexpr uint32_t TOTAL = META + 4 * (4 * CST + SCS + 2);
   static constexpr uint32_t BYTES = TOTAL + 1024;
 };
 static_assert(TqSmem<128>::BYTES <= 232448, "shared memory");
@@ -111,10 +115,10 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + SM::BARS);
-  volatile int* meta = reinterpret_cast<volatile int*>(sm + SM::META);          // [CST][2]: the block is there
-  volatile int* sc_ok = meta + 2 * CST;                                         // [SCS]: the same, two bits
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + SM::META) + 2 * CST + SCS;
-  volatile int* abort_flag = meta + 2 * CST + SCS + 1;
+  volatile int* meta = reinterpret_cast<volatile int*>(sm + SM::META);          // [2 CST][2]: the block is there
+  volatile int* sc_ok = meta + 4 * CST;                                         // [SCS]: the same, two bits
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + SM::META) + 4 * CST + SCS;
+  volatile int* abort_flag = meta + 4 * CST + SCS + 1;
   __shared__ Q4Start start_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -174,45 +178,43 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
     }
     if (warp == 0) {
       // ------------------------------------------------------------- slots' bytes
-      int n = 0;   // step
-      bool stop = false;
+      int n = 0;   // step (lane 0 brings K codes, lane 1 V codes, each at its ring's pace)
       for (int k = 0;; ++k) {
         const TqPiece walk = told(k);
         if (!walk.more) break;
-        const int* row = p.table + (size_t)walk.r * p.table_ld;
-        for (int b0 = walk.b0; b0 < walk.b1 && !stop; b0 += 32) {
-          const int mine = b0 + lane < walk.b1 ? __ldg(row + b0 + lane) : -1;
-          const int cnt = min(32, walk.b1 - b0);
-          for (int i = 0; i < cnt && !stop; i += 2) {
-            const int slot0 = __shfl_sync(0xffffffffu, mine, i), slot1 = __shfl_sync(0xffffffffu, mine, i + 1);
-            const int cs = n % CST;
-            if (lane == 0) {
-              wait(T_CEMPTY + cs, ((n / CST) & 1) ^ 1);
-              if (!*abort_flag) {
-                const bool has1 = i + 1 < cnt;
-                const bool ok0 = slot0 >= 0 && slot0 < p.pool_slots, ok1 = has1 && slot1 >= 0 && slot1 < p.pool_slots;
-                if (!ok0) record_error(p.ws, PBSA_ERR_DEVICE_INDEX, slot0, K_Q4_ATTEND);
-                if (has1 && !ok1) record_error(p.ws, PBSA_ERR_DEVICE_INDEX, slot1, K_Q4_ATTEND);
-                meta[2 * cs] = ok0;
-                meta[2 * cs + 1] = ok1;
-                uint8_t* dst = sm + SM::CODES + cs * SM::STEP;
-                const uint8_t* src = p.pool + (size_t)walk.h * p.pool_slots * Q::BYTES;
-                const uint32_t bytes = (ok0 ? Q::BYTES : 0) + (ok1 ? Q::BYTES : 0);
-                if (bytes > 0) mbar_arrive_expect_tx(&bars[T_CFULL + cs], bytes);
-                else mbar_arrive(&bars[T_CFULL + cs]);
-                if (ok0) bulk_load(dst, src + (size_t)slot0 * Q::BYTES, Q::BYTES, &bars[T_CFULL + cs]);
-                if (ok1) bulk_load(dst + Q::BYTES, src + (size_t)slot1 * Q::BYTES, Q::BYTES, &bars[T_CFULL + cs]);
-                ++n;
-              }
-            }
-            n = __shfl_sync(0xffffffffu, n, 0);
-            stop = __any_sync(0xffffffffu, *abort_flag != 0);
+        if (lane < 2) {
+          const int* row = p.table + (size_t)walk.r * p.table_ld;
+          const uint8_t* src = p.pool + (size_t)walk.h * p.pool_slots * Q::BYTES + lane * Q::HALF;
+          int next0 = walk.b0 < walk.b1 ? __ldg(row + walk.b0) : -1;
+          int next1 = walk.b0 + 1 < walk.b1 ? __ldg(row + walk.b0 + 1) : -1;
+          for (int b = walk.b0; b < walk.b1 && !*abort_flag; b += 2) {
+            const int slot0 = next0, slot1 = next1;
+            const bool has1 = b + 1 < walk.b1;
+            if (b + 2 < walk.b1) next0 = __ldg(row + b + 2);
+            if (b + 3 < walk.b1) next1 = __ldg(row + b + 3);
+            const int cs = lane * CST + n % CST;
+            wait(T_CEMPTY + cs, ((n / CST) & 1) ^ 1);
+            if (*abort_flag) break;
+            const bool ok0 = slot0 >= 0 && slot0 < p.pool_slots, ok1 = has1 && slot1 >= 0 && slot1 < p.pool_slots;
+            if (!ok0) record_error(p.ws, PBSA_ERR_DEVICE_INDEX, slot0, K_Q4_ATTEND);
+            if (has1 && !ok1) record_error(p.ws, PBSA_ERR_DEVICE_INDEX, slot1, K_Q4_ATTEND);
+            meta[2 * cs] = ok0;
+            meta[2 * cs + 1] = ok1;
+            uint8_t* dst = sm + SM::CODES + cs * SM::STEP;
+            const uint32_t bytes = (ok0 ? Q::HALF : 0) + (ok1 ? Q::HALF : 0);
+            if (bytes > 0) mbar_arrive_expect_tx(&bars[T_CFULL + cs], bytes);
+            else mbar_arrive(&bars[T_CFULL + cs]);
+            if (ok0) bulk_load(dst, src + (size_t)slot0 * Q::BYTES, Q::HALF, &bars[T_CFULL + cs]);
+            if (ok1) bulk_load(dst + Q::HALF, src + (size_t)slot1 * Q::BYTES, Q::HALF, &bars[T_CFULL + cs]);
+            ++n;
           }
         }
+        __syncwarp();
       }
       // the CTA must not end with copies in flight
-      if (lane == 0)
-        for (int i = max(0, n - CST); i < n; ++i) mbar_wait(&bars[T_CFULL + i % CST], (i / CST) & 1, kWaitLimitNs);
+      if (lane < 2)
+        for (int i = max(0, n - CST); i < n; ++i)
+          mbar_wait(&bars[T_CFULL + lane * CST + i % CST], (i / CST) & 1, kWaitLimitNs);
       __syncwarp();
     }
     if (warp == 1 || warp == 3) {
@@ -305,29 +307,18 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
         fence_proxy_async_smem();
         mbar_arrive(&bars[T_QFULL]);
       }
-      const int n1 = n + ((walk.b1 - walk.b0 + 1) >> 1), first = n;
-      for (n += (n ^ ug) & 1; n < n1; n += 2) {
-        const int b = walk.b0 + 2 * (n - first);
-        const int cs = n % CST, sk = n % KST, sv = n % VST;
+      const int n1 = n + ((walk.b1 - walk.b0 + 1) >> 1), start = n, first = n + ((n ^ ug) & 1);
+      auto unpack_k = [&](int n) {
+        const int cs = n % CST, sk = n % KST;
         wait(T_CFULL + cs, (n / CST) & 1);
         const uint8_t* codes = sm + SM::CODES + cs * SM::STEP;
-        const bool ok0 = meta[2 * cs] != 0, ok1 = meta[2 * cs + 1] != 0;
-        {   // scale and offset of key t, in log2 units
-          const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + (t >> 6) * Q::BYTES + Q::OFF_KS + (t & 63) * 4);
-          float* sc = reinterpret_cast<float*>(sm + SM::SC) + (n % SCS) * 256;
-          const float s = lo_bf16(w);
-          sc[t] = s * p.scale_log2;
-          sc[128 + t] = fmaf(-128.f, s, hi_bf16(w)) * p.scale_log2;
-          if (t == 0) sc_ok[n % SCS] = (ok0 ? 1 : 0) | (ok1 ? 2 : 0);
-          mbar_arrive(&bars[T_SCFULL + n % SCS]);
-        }
         // K: 16 (D = 64: 8) code bytes a lane; 8 lanes write 4 rows of two neighbouring column groups, 8
         // different 16-byte columns after the swizzle.  All of a thread's codes are read before the first is used.
         {
           constexpr int W = Q::WORDS;                   // words of a lane's bytes; 4 lanes a row
           const int row8 = ((lane >> 4) & 1) * 4 + ((lane >> 1) & 3), j = ((lane >> 3) & 1) * 2 + (lane & 1);
           const int row0 = uw * 32 + row8;              // key of the step; + 8 a turn
-          const uint8_t* src = codes + (uw >> 1) * Q::BYTES + (row0 & 63) * Q::KROW + j * Q::LANE;
+          const uint8_t* src = codes + (uw >> 1) * Q::HALF + (row0 & 63) * Q::KROW + j * Q::LANE;
           uint32_t w[4][W];
 #pragma unroll
           for (int it = 0; it < 4; ++it) {
@@ -340,7 +331,16 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
             }
           }
           uint8_t* dst = sm + SM::K + sk * SM::TILE + ((j * W) >> 3) * 16384 + row0 * 128;
-          wait(T_KEMPTY + sk, ((n / KST) & 1) ^ 1);
+          wait(T_KEMPTY + sk, ((n / KST) & 1) ^ 1);   // QK(n-2) is done, and before it the softmax of step n-4
+          {   // scale and offset of key t, in log2 units
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + (t >> 6) * Q::HALF + Q::OFF_KS + (t & 63) * 4);
+            float* sc = reinterpret_cast<float*>(sm + SM::SC) + (n % SCS) * 256;
+            const float s = lo_bf16(w);
+            sc[t] = s * p.scale_log2;
+            sc[128 + t] = fmaf(-128.f, s, hi_bf16(w)) * p.scale_log2;
+            if (t == 0) sc_ok[n % SCS] = (meta[2 * cs] ? 1 : 0) | (meta[2 * cs + 1] ? 2 : 0);
+            mbar_arrive(&bars[T_SCFULL + n % SCS]);
+          }
 #pragma unroll
           for (int i = 0; i < W; ++i) {
             const int at = (((j * W + i) & 7) ^ row8) << 4;   // 16-byte column, swizzled
@@ -351,7 +351,16 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
           }
           fence_proxy_async_smem();
           mbar_arrive(&bars[T_KFULL + sk]);
+          mbar_arrive(&bars[T_CEMPTY + cs]);
         }
+      };
+      if (first < n1) unpack_k(first);
+      for (n = first; n < n1; n += 2) {
+        if (n + 2 < n1) unpack_k(n + 2);   // V(n) may have to wait for PV(n-2); the next S does not
+        const int b = walk.b0 + 2 * (n - start), cs = CST + n % CST, sv = n % VST;
+        wait(T_CFULL + cs, (n / CST) & 1);
+        const uint8_t* codes = sm + SM::CODES + cs * SM::STEP;
+        const bool ok0 = meta[2 * cs] != 0, ok1 = meta[2 * cs + 1] != 0;
         // V: 8 channels of two tokens a lane and turn, a block's turns together
         {
           constexpr int HALVES = D / 64;                // 8-channel halves of a lane's bytes in the layout
@@ -363,13 +372,13 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
           uint8_t* dst = sm + SM::V + sv * SM::TILE + (col >> 3) * 16384 + row0 * 128;
 #pragma unroll 1
           for (int half = 0; half < 2; ++half) {
-            const uint8_t* blk = codes + half * Q::BYTES;
-            const uint8_t* src = blk + Q::OFF_V + (u8 * 32 + g * 4 + j) * Q::LANE + 8 * k;
+            const uint8_t* blk = codes + half * Q::HALF;
+            const uint8_t* src = blk + (u8 * 32 + g * 4 + j) * Q::LANE + 8 * k;
             uint2 w[TURNS], sc[TURNS];
 #pragma unroll
             for (int i = 0; i < TURNS; ++i) {
               w[i] = *reinterpret_cast<const uint2*>(src + i * GROUPS * 32 * Q::LANE);
-              sc[i] = *reinterpret_cast<const uint2*>(blk + Q::OFF_VS + (row0 + i * GROUPS * 8) * 4);
+              sc[i] = *reinterpret_cast<const uint2*>(blk + Q::CODE + (row0 + i * GROUPS * 8) * 4);
             }
             // tokens of this block that are cached (none of a block that is not there)
             const int left = (half ? ok1 : ok0) ? walk.kv_len - (b + half) * BT : 0;

@@ -14,11 +14,13 @@
 //   K codes  [64 tokens][D/2 bytes]: 32-bit word w of a token holds channels 8w .. 8w+7, channel
 //            8w + 2i in nibble i and 8w + 2i + 1 in nibble i + 4, so (word >> 4i) & 0x000F000F is a
 //            pair of neighbouring channels in the two halves of a register.
+//   K (s, m) [64] pairs of bf16 (s in the low half).
 //   V codes  pairs along tokens, as the second product contracts over tokens: units of 16 tokens,
 //            [unit u][half ph][g 0..7][j 0..3][D/8 bytes], tokens 16u + 8ph + 2j (low half words) and
 //            + 1 (high half words); 32-bit word w holds channels (D/8) g + 4w + n in nibble n of
 //            each half word.
-//   K (s, m) [64] pairs of bf16 (s in the low half);  V (s, m) [64] likewise.
+//   V (s, m) [64] pairs of bf16.
+// The K half and the V half of a slot are equally long and can be copied apart.
 #pragma once
 #include "common.cuh"
 
@@ -27,10 +29,11 @@ namespace pbsa {
 template <int D>
 struct Q4 {
   static constexpr int CODE = BT * D / 2;          // bytes of K (or V) codes of a slot
-  static constexpr int OFF_V = CODE;
-  static constexpr int OFF_KS = 2 * CODE;
-  static constexpr int OFF_VS = OFF_KS + BT * 4;
-  static constexpr int BYTES = OFF_VS + BT * 4;
+  static constexpr int HALF = CODE + BT * 4;       // K, or V, with its scales and minima
+  static constexpr int OFF_KS = CODE;
+  static constexpr int OFF_V = HALF;
+  static constexpr int OFF_VS = HALF + CODE;
+  static constexpr int BYTES = 2 * HALF;
   static constexpr int KROW = D / 2;               // bytes of a token's K codes
   static constexpr int UNIT = 16 * D / 2;          // bytes of V codes of 16 tokens
   static constexpr int LANE = D / 8;               // bytes of one thread's fragment words
