@@ -308,11 +308,23 @@ def pbsa_attend_bwd(g: Geom, q, q_frames, k_pool, v_pool, pool_slots, kv_slot, k
 PBSA_CAUSAL = 1
 
 
-def _dev(t, dtype, name, numel=None, index=None):
-    """Device pointer (an int) of a contiguous tensor of the call's device: `index` is the first tensor's."""
-    if t is None:
-        return None
-    if not t.is_cuda or t.get_device() != index:
+# These calls are made per layer and step, so the checks are kept to a few attribute reads a tensor.
+_I32 = torch.int32
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # the current stream's handle, without a Stream object
+_Q4_SIZES = {}                                                       # head_dim -> (bytes of a slot, of the workspace)
+
+
+def _call_env(stream):
+    """(current device, its stream's handle) of a call."""
+    dev = torch.cuda.current_device()
+    if stream is not None:
+        return dev, stream.cuda_stream
+    return dev, _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+
+
+def _dev(t, dtype, name, numel, index):
+    """Device pointer (an int) of a contiguous tensor of device ``index`` (of ``numel`` elements, unless None)."""
+    if t.get_device() != index:
         raise ValueError(f"{name} must be a tensor of the current CUDA device")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
@@ -325,30 +337,27 @@ def _dev(t, dtype, name, numel=None, index=None):
 
 def _tokens(t, dtype, name, heads, d, index):
     """(pointer, elements between tokens, tokens) of [tokens, heads, d] whose tokens may lie apart."""
-    if not t.is_cuda or t.get_device() != index:
+    if t.get_device() != index:
         raise ValueError(f"{name} must be a tensor of the current CUDA device")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
-        raise ValueError(f"{name} must be [tokens, {heads}, {d}], got {list(t.shape)}")
-    n = t.shape[0]
-    if n and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d:
+        raise ValueError(f"{name} must be [tokens, {heads}, {d}], got {list(shape)}")
+    n, (ld, sh, se) = shape[0], t.stride()
+    if n and (se != 1 or (heads > 1 and sh != d)):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), (t.stride(0) if n > 1 else heads * d), n
+    return t.data_ptr(), (ld if n > 1 else heads * d), n
 
 
 def _ws(ws, index, need=256):
     if ws is None:
         return None
-    if not ws.is_cuda or ws.get_device() != index:
+    if ws.get_device() != index:
         raise ValueError("ws must be a tensor of the current CUDA device")
     if not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
         raise ValueError(f"ws must be contiguous and hold {need} bytes")
     return ws.data_ptr()
-
-
-def _st(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
 
 
 def pbsa_q4_block_bytes(g: ReqGeom) -> int:
@@ -359,61 +368,77 @@ def pbsa_attend_q4_workspace_bytes(g: ReqGeom) -> int:
     return int(load().pbsa_attend_q4_workspace_bytes(ctypes.byref(g)))
 
 
-def _q4_pool(g, pool, pool_slots, index):
-    return _dev(pool, torch.uint8, "pool", g.kv_heads * pool_slots * pbsa_q4_block_bytes(g), index)
+def _q4_sizes(g):
+    """Both sizes, which depend on head_dim alone, asked once (0 for a geometry that the call then refuses)."""
+    hit = _Q4_SIZES.get(g.head_dim)
+    if hit is None:
+        hit = (pbsa_q4_block_bytes(g), pbsa_attend_q4_workspace_bytes(g))
+        if hit[0]:
+            _Q4_SIZES[g.head_dim] = hit
+    return hit
 
 
 def _rows(t, name):
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{name} must be two-dimensional")
-    return t.shape
+    return shape
 
 
 def pbsa_request_tables(step_len, seq_len, block_table, free_slot, free_cnt, q_start, q_len, kv_len, free_cnt_out,
                         slot_map, position=None, ws=None, stream=None):
     """Sizes are the tensors': requests of ``step_len``, table_ld of ``block_table`` [requests, table_ld], slots
     of ``free_slot``, tokens of ``slot_map``."""
-    i32, dev = torch.int32, torch.cuda.current_device()
+    dev, st = _call_env(stream)
     R, ld = _rows(block_table, "block_table")
     T, S = slot_map.numel(), free_slot.numel()
-    _check("pbsa_request_tables", load().pbsa_request_tables(
-        _dev(step_len, i32, "step_len", R, dev), _dev(seq_len, i32, "seq_len", R, dev), R,
-        _dev(block_table, i32, "block_table", None, dev), ld, _dev(free_slot, i32, "free_slot", None, dev),
-        _dev(free_cnt, i32, "free_cnt", 1, dev), S, T, _dev(q_start, i32, "q_start", R + 1, dev),
-        _dev(q_len, i32, "q_len", R, dev), _dev(kv_len, i32, "kv_len", R, dev),
-        _dev(free_cnt_out, i32, "free_cnt_out", 1, dev), _dev(slot_map, i32, "slot_map", None, dev) if T else None,
-        _dev(position, i32, "position", T, dev), _ws(ws, dev), _st(stream)))
+    code = load().pbsa_request_tables(
+        _dev(step_len, _I32, "step_len", R, dev), _dev(seq_len, _I32, "seq_len", R, dev), R,
+        _dev(block_table, _I32, "block_table", None, dev), ld, _dev(free_slot, _I32, "free_slot", None, dev),
+        _dev(free_cnt, _I32, "free_cnt", 1, dev), S, T, _dev(q_start, _I32, "q_start", R + 1, dev),
+        _dev(q_len, _I32, "q_len", R, dev), _dev(kv_len, _I32, "kv_len", R, dev),
+        _dev(free_cnt_out, _I32, "free_cnt_out", 1, dev), _dev(slot_map, _I32, "slot_map", None, dev) if T else None,
+        None if position is None else _dev(position, _I32, "position", T, dev), _ws(ws, dev), st)
+    if code:
+        raise PBSAError("pbsa_request_tables", code)
 
 
 def pbsa_append_q4(g: ReqGeom, k, v, slot_map, pool, pool_slots, ws=None, stream=None):
     """``k``, ``v`` [tokens, kv_heads, head_dim]; tokens may lie apart (a slice of a projection's output)."""
-    dt, dev = _tok_dtype(g), torch.cuda.current_device()
-    kp, kl, n = _tokens(k, dt, "k", g.kv_heads, g.head_dim, dev)
-    vp, vl, m = _tokens(v, dt, "v", g.kv_heads, g.head_dim, dev)
+    dev, st = _call_env(stream)
+    dt, H, d = _tok_dtype(g), g.kv_heads, g.head_dim
+    kp, kl, n = _tokens(k, dt, "k", H, d, dev)
+    vp, vl, m = _tokens(v, dt, "v", H, d, dev)
     if m != n:
         raise ValueError("k and v must have the same number of tokens")
-    _check("pbsa_append_q4", load().pbsa_append_q4(
-        g, kp, kl, vp, vl, n, _dev(slot_map, torch.int32, "slot_map", n, dev), _q4_pool(g, pool, pool_slots, dev),
-        pool_slots, _ws(ws, dev), _st(stream)))
+    code = load().pbsa_append_q4(
+        g, kp, kl, vp, vl, n, _dev(slot_map, _I32, "slot_map", n, dev),
+        _dev(pool, torch.uint8, "pool", H * pool_slots * _q4_sizes(g)[0], dev), pool_slots, _ws(ws, dev), st)
+    if code:
+        raise PBSAError("pbsa_append_q4", code)
 
 
 def pbsa_expand_q4(g: ReqGeom, pool, pool_slots, src_slot, k_pool, v_pool, ws=None, stream=None):
     """``k_pool``, ``v_pool`` [kv_heads, len(src_slot), 64, head_dim]."""
-    dt, dev = _tok_dtype(g), torch.cuda.current_device()
-    n = src_slot.numel()
-    size = g.kv_heads * n * 64 * g.head_dim
-    _check("pbsa_expand_q4", load().pbsa_expand_q4(
-        g, _q4_pool(g, pool, pool_slots, dev), pool_slots, _dev(src_slot, torch.int32, "src_slot", None, dev), n,
-        _dev(k_pool, dt, "k_pool", size, dev), _dev(v_pool, dt, "v_pool", size, dev), _ws(ws, dev), _st(stream)))
+    dev, st = _call_env(stream)
+    dt, H, d, n = _tok_dtype(g), g.kv_heads, g.head_dim, src_slot.numel()
+    size = H * n * 64 * d
+    code = load().pbsa_expand_q4(
+        g, _dev(pool, torch.uint8, "pool", H * pool_slots * _q4_sizes(g)[0], dev), pool_slots,
+        _dev(src_slot, _I32, "src_slot", None, dev), n, _dev(k_pool, dt, "k_pool", size, dev),
+        _dev(v_pool, dt, "v_pool", size, dev), _ws(ws, dev), st)
+    if code:
+        raise PBSAError("pbsa_expand_q4", code)
 
 
 def pbsa_attend_q4(g: ReqGeom, q, q_start, q_len, kv_len, max_q_len, pool, pool_slots, block_table, causal, o,
                    lse=None, ws=None, stream=None):
     """``q``, ``o`` [tokens, q_heads, head_dim]; tokens may lie apart.  ``q_start`` holds one entry per request or
     one more (as pbsa_request_tables writes it)."""
-    dt, i32, dev = _tok_dtype(g), torch.int32, torch.cuda.current_device()
-    qp, ql, n = _tokens(q, dt, "q", g.q_heads, g.head_dim, dev)
-    op, ol, m = _tokens(o, dt, "o", g.q_heads, g.head_dim, dev)
+    dev, st = _call_env(stream)
+    dt, Hq, d = _tok_dtype(g), g.q_heads, g.head_dim
+    qp, ql, n = _tokens(q, dt, "q", Hq, d, dev)
+    op, ol, m = _tokens(o, dt, "o", Hq, d, dev)
     if m != n:
         raise ValueError("o must have q's tokens")
     R, ld = _rows(block_table, "block_table")
@@ -421,12 +446,15 @@ def pbsa_attend_q4(g: ReqGeom, q, q_start, q_len, kv_len, max_q_len, pool, pool_
         raise ValueError(f"q_start must have {R} or {R + 1} elements, got {q_start.numel()}")
     if ws is None:
         raise ValueError("pbsa_attend_q4 needs a workspace")
-    _check("pbsa_attend_q4", load().pbsa_attend_q4(
-        g, qp, ql, n, _dev(q_start, i32, "q_start", None, dev), _dev(q_len, i32, "q_len", R, dev),
-        _dev(kv_len, i32, "kv_len", R, dev), R, max_q_len, _q4_pool(g, pool, pool_slots, dev), pool_slots,
-        _dev(block_table, i32, "block_table", None, dev), ld, PBSA_CAUSAL if causal else 0, op, ol,
-        _dev(lse, torch.float32, "lse", g.q_heads * n, dev),
-        _ws(ws, dev, pbsa_attend_q4_workspace_bytes(g)), _st(stream)))
+    block, need = _q4_sizes(g)
+    code = load().pbsa_attend_q4(
+        g, qp, ql, n, _dev(q_start, _I32, "q_start", None, dev), _dev(q_len, _I32, "q_len", R, dev),
+        _dev(kv_len, _I32, "kv_len", R, dev), R, max_q_len,
+        _dev(pool, torch.uint8, "pool", g.kv_heads * pool_slots * block, dev), pool_slots,
+        _dev(block_table, _I32, "block_table", None, dev), ld, PBSA_CAUSAL if causal else 0, op, ol,
+        None if lse is None else _dev(lse, torch.float32, "lse", Hq * n, dev), _ws(ws, dev, need), st)
+    if code:
+        raise PBSAError("pbsa_attend_q4", code)
 
 
 def pbsa_selftest_wait_timeout(ws, limit_us: int, stream=None):
