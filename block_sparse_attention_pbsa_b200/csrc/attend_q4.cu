@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(AQ_THREADS) attend_q4_kernel(const AttendQ4Par
           const int slot = __shfl_sync(0xffffffffu, mine, i);
           if (lane == 0 && !*abort_flag) {
             const int s = issued % AQ_STAGES;
-            if (!mbar_wait(&empty[s], ((issued / AQ_STAGES) & 1) ^ 1, kWaitLimitNs)) {
+            if (!mbar_wait_parked(&empty[s], ((issued / AQ_STAGES) & 1) ^ 1, kWaitLimitNs)) {
               record_error(p.ws, PBSA_ERR_TIMEOUT, issued, K_Q4_ATTEND);
               *abort_flag = 1;
             } else {
@@ -205,11 +205,12 @@ __global__ void __launch_bounds__(AQ_THREADS) attend_q4_kernel(const AttendQ4Par
     }
     const int lim_min = p.causal ? max(walk.kv_len - walk.q_len + row0 / p.group + 1, 0) : walk.kv_len;
 
-    float o[NT][D / 16][4], ref[NT][2], l[NT][2], pm[NT][2];
+    // A column's reference is `sub` once a key has been seen (`over`, 2^8 above it, is -inf until then).
+    float o[NT][D / 16][4], sub[NT][2], over[NT][2], l[NT][2], pm[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) { ref[nt][i] = -INFINITY; l[nt][i] = 0.f; pm[nt][i] = 0.f; }
+      for (int i = 0; i < 2; ++i) { over[nt][i] = -INFINITY; sub[nt][i] = l[nt][i] = pm[nt][i] = 0.f; }
 #pragma unroll
       for (int mt = 0; mt < D / 16; ++mt)
 #pragma unroll
@@ -218,11 +219,13 @@ __global__ void __launch_bounds__(AQ_THREADS) attend_q4_kernel(const AttendQ4Par
 
     for (int b = walk.b0; b < walk.b1; ++b, ++taken) {
       const int s = taken % AQ_STAGES;
-      if (!*abort_flag && !mbar_wait(&full[s], (taken / AQ_STAGES) & 1, kWaitLimitNs)) {
+      // (after an abort the loop runs on without waiting: the barriers at the tile's end have all warps)
+      if (!mbar_try_wait(&full[s], (taken / AQ_STAGES) & 1) && !*abort_flag &&
+          !mbar_wait_parked(&full[s], (taken / AQ_STAGES) & 1, kWaitLimitNs)) {
         record_error(p.ws, PBSA_ERR_TIMEOUT, taken, K_Q4_ATTEND);
         *abort_flag = 1;
       }
-      if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+      __syncwarp();
       const uint8_t* blk = sm + s * Q::BYTES;
       const int t0 = b * BT + warp * 16;               // first of this warp's 16 tokens
       if (meta[s] != 0 && t0 < walk.kv_len) {
@@ -290,7 +293,7 @@ __global__ void __launch_bounds__(AQ_THREADS) attend_q4_kernel(const AttendQ4Par
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) grow |= fmaxf(x[nt][i], x[nt][i + 2]) > ref[nt][i] + 8.f;
+          for (int i = 0; i < 2; ++i) grow |= fmaxf(x[nt][i], x[nt][i + 2]) > over[nt][i];
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -300,10 +303,11 @@ __global__ void __launch_bounds__(AQ_THREADS) attend_q4_kernel(const AttendQ4Par
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-              if (mx > ref[nt][i] + 8.f) {
-                // (nothing but zeros was summed against -inf)
-                const float al = ref[nt][i] == -INFINITY ? 1.f : ex2_approx(ref[nt][i] - mx);
-                ref[nt][i] = mx;
+              if (mx > over[nt][i]) {
+                // (nothing but zeros was summed before the first key)
+                const float al = over[nt][i] == -INFINITY ? 1.f : ex2_approx(sub[nt][i] - mx);
+                sub[nt][i] = mx;
+                over[nt][i] = mx + 8.f;
                 l[nt][i] *= al;
                 pm[nt][i] *= al;
 #pragma unroll
@@ -316,10 +320,7 @@ __global__ void __launch_bounds__(AQ_THREADS) attend_q4_kernel(const AttendQ4Par
         for (int nt = 0; nt < NT; ++nt) {
           float e[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            e[i] = ex2_approx(x[nt][i] - ref[nt][i & 1]);
-            if (masked && x[nt][i] == -INFINITY) e[i] = 0.f;   // (-inf less a reference of -inf)
-          }
+          for (int i = 0; i < 4; ++i) e[i] = ex2_approx(x[nt][i] - sub[nt][i & 1]);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             l[nt][i] += e[i] + e[i + 2];
@@ -368,7 +369,7 @@ __global__ void __launch_bounds__(AQ_THREADS) attend_q4_kernel(const AttendQ4Par
           pm[nt][i] += __shfl_xor_sync(0xffffffffu, pm[nt][i], s2);
         }
         const int col = nt * 8 + 2 * j + i;
-        if (g == 0) ex_ml[warp * ROWS + col] = make_float2(ref[nt][i], l[nt][i]);
+        if (g == 0) ex_ml[warp * ROWS + col] = make_float2(over[nt][i] == -INFINITY ? -INFINITY : sub[nt][i], l[nt][i]);
         float* dst = ex_o + (size_t)(warp * ROWS + col) * SM::OSTRIDE + g * (D / 8);
 #pragma unroll
         for (int mt = 0; mt < D / 16; mt += 2) {

@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
   const uint32_t tmem = *tmem_holder;
   auto wait = [&](int bar, uint32_t parity) {
     if (*abort_flag) return;
-    if (!mbar_wait(&bars[bar], parity, kWaitLimitNs)) {
+    if (!mbar_wait_parked(&bars[bar], parity, kWaitLimitNs)) {
       record_error(p.ws, PBSA_ERR_TIMEOUT, bar, K_Q4_ATTEND);
       *abort_flag = 1;
     }
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
 
   // The k-th piece, for a whole warp (not cut short by an abort: every role goes through every piece).
   auto told = [&](int k) {
-    if (!mbar_wait(&bars[T_WFULL + (k & 1)], (k >> 1) & 1, 2 * kWaitLimitNs)) *abort_flag = 1;
+    if (!mbar_wait_parked(&bars[T_WFULL + (k & 1)], (k >> 1) & 1, 2 * kWaitLimitNs)) *abort_flag = 1;
     const TqPiece w = reinterpret_cast<const TqPiece*>(sm + SM::WALK)[k & 1];
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars[T_WEMPTY + (k & 1)]);
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
         bool more = true;
         for (int k = 0; more; ++k) {
           more = walk.next();
-          if (!mbar_wait(&bars[T_WEMPTY + (k & 1)], ((k >> 1) & 1) ^ 1, 2 * kWaitLimitNs)) *abort_flag = 1;
+          if (!mbar_wait_parked(&bars[T_WEMPTY + (k & 1)], ((k >> 1) & 1) ^ 1, 2 * kWaitLimitNs)) *abort_flag = 1;
           reinterpret_cast<TqPiece*>(sm + SM::WALK)[k & 1] = {more ? 1 : 0, walk.r, walk.b0, walk.b1, walk.mt, walk.h,
                                                              walk.q0, walk.q_len, walk.kv_len, walk.rows, walk.piece, 0};
           mbar_arrive(&bars[T_WFULL + (k & 1)]);

@@ -45,6 +45,25 @@ struct Q4 {
   }
 };
 
+// As mbar_wait, for waits that are expected to last: the thread is parked by the hardware for up to 20 us at a
+// time instead of polling, which would take issue slots from the warps that have work.
+__device__ __forceinline__ bool mbar_wait_parked(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    if (ok) return true;
+    if (global_timer_ns() - t0 > limit_ns) return false;
+  }
+}
+
 // min and max that return NaN if either operand is NaN
 __device__ __forceinline__ float min_nan(float a, float b) {
   float d;
