@@ -19,7 +19,7 @@
 //    partial (o, maximum, sum) per piece, and a second kernel, launched as a programmatic dependent,
 //    joins the pieces in order.  At most one tile starts in a CTA and ends in a later one, so a CTA
 //    has two slots for pieces.  Nothing carries over from call to call.
-//  * A producer warp brings whole slots (8704 bytes: K, V, scales) with one bulk copy each into a ring;
+//  * A producer warp brings whole slots (8704 bytes: K, V, scales) with one bulk copy each into a ring of pairs;
 //    four warps take 16 tokens of each slot, with a running maximum and sum of their own, joined
 //    in shared memory at a tile's end.  The reference maximum moves only when a score exceeds it by
 //    2^8, which one vote per 16 tokens detects.
@@ -38,18 +38,18 @@ namespace {
 
 constexpr int AQ_WARPS = 4;                       // computing warps
 constexpr int AQ_THREADS = (AQ_WARPS + 1) * 32;   // + the producer
-constexpr int AQ_STAGES = 6;
+constexpr int AQ_STAGES = 3;                      // of two slots each
 constexpr int AQ_MIN_STEPS = 2;                   // blocks that are worth a CTA of their own
 
 template <int D, int NT>
 struct AqSmem {
   static constexpr int ROWS = 8 * NT;
   static constexpr int OSTRIDE = D + 4;
-  static constexpr int RING = AQ_STAGES * Q4<D>::BYTES;
+  static constexpr int RING = AQ_STAGES * 2 * Q4<D>::BYTES;
   static constexpr int EX_O = RING;                                      // float[4][ROWS][OSTRIDE]
   static constexpr int EX_ML = EX_O + AQ_WARPS * ROWS * OSTRIDE * 4;     // float2[4][ROWS]
   static constexpr int BARS = EX_ML + AQ_WARPS * ROWS * 8;               // full, empty
-  static constexpr int META = BARS + 2 * AQ_STAGES * 8;                  // int[stages]: block present
+  static constexpr int META = BARS + 2 * AQ_STAGES * 8;                  // int[stages]: slots present (two bits)
   static constexpr int TOTAL = META + AQ_STAGES * 4 + 16;
 };
 
@@ -113,23 +113,26 @@ __global__ void __launch_bounds__(AQ_THREADS) attend_q4_kernel(const AttendQ4Par
       for (int b0 = walk.b0; b0 < walk.b1 && !stop; b0 += 32) {
         const int mine = b0 + lane < walk.b1 ? __ldg(row + b0 + lane) : -1;
         const int n = min(32, walk.b1 - b0);
-        for (int i = 0; i < n && !stop; ++i) {
-          const int slot = __shfl_sync(0xffffffffu, mine, i);
+        for (int i = 0; i < n && !stop; i += 2) {
+          const int slot0 = __shfl_sync(0xffffffffu, mine, i), slot1 = __shfl_sync(0xffffffffu, mine, (i + 1) & 31);
           if (lane == 0 && !*abort_flag) {
             const int s = issued % AQ_STAGES;
             if (!mbar_wait_parked(&empty[s], ((issued / AQ_STAGES) & 1) ^ 1, kWaitLimitNs)) {
               record_error(p.ws, PBSA_ERR_TIMEOUT, issued, K_Q4_ATTEND);
               *abort_flag = 1;
             } else {
-              if (slot >= 0 && slot < p.pool_slots) {
-                meta[s] = 1;
-                mbar_arrive_expect_tx(&full[s], Q::BYTES);
-                bulk_load(sm + s * Q::BYTES, p.pool + ((size_t)walk.h * p.pool_slots + slot) * Q::BYTES, Q::BYTES, &full[s]);
-              } else {
-                record_error(p.ws, PBSA_ERR_DEVICE_INDEX, slot, K_Q4_ATTEND);
-                meta[s] = 0;
-                mbar_arrive(&full[s]);
-              }
+              const bool has1 = i + 1 < n;
+              const bool ok0 = slot0 >= 0 && slot0 < p.pool_slots, ok1 = has1 && slot1 >= 0 && slot1 < p.pool_slots;
+              if (!ok0) record_error(p.ws, PBSA_ERR_DEVICE_INDEX, slot0, K_Q4_ATTEND);
+              if (has1 && !ok1) record_error(p.ws, PBSA_ERR_DEVICE_INDEX, slot1, K_Q4_ATTEND);
+              meta[s] = (ok0 ? 1 : 0) | (ok1 ? 2 : 0);
+              uint8_t* dst = sm + s * 2 * Q::BYTES;
+              const uint8_t* src = p.pool + (size_t)walk.h * p.pool_slots * Q::BYTES;
+              const uint32_t bytes = (ok0 ? Q::BYTES : 0) + (ok1 ? Q::BYTES : 0);
+              if (bytes > 0) mbar_arrive_expect_tx(&full[s], bytes);
+              else mbar_arrive(&full[s]);
+              if (ok0) bulk_load(dst, src + (size_t)slot0 * Q::BYTES, Q::BYTES, &full[s]);
+              if (ok1) bulk_load(dst + Q::BYTES, src + (size_t)slot1 * Q::BYTES, Q::BYTES, &full[s]);
               ++issued;
             }
           }
@@ -217,7 +220,7 @@ __global__ void __launch_bounds__(AQ_THREADS) attend_q4_kernel(const AttendQ4Par
         for (int i = 0; i < 4; ++i) o[nt][mt][i] = 0.f;
     }
 
-    for (int b = walk.b0; b < walk.b1; ++b, ++taken) {
+    for (int b = walk.b0; b < walk.b1; b += 2, ++taken) {
       const int s = taken % AQ_STAGES;
       // (after an abort the loop runs on without waiting: the barriers at the tile's end have all warps)
       if (!mbar_try_wait(&full[s], (taken / AQ_STAGES) & 1) && !*abort_flag &&
@@ -226,9 +229,12 @@ __global__ void __launch_bounds__(AQ_THREADS) attend_q4_kernel(const AttendQ4Par
         *abort_flag = 1;
       }
       __syncwarp();
-      const uint8_t* blk = sm + s * Q::BYTES;
-      const int t0 = b * BT + warp * 16;               // first of this warp's 16 tokens
-      if (meta[s] != 0 && t0 < walk.kv_len) {
+      const int here = meta[s];
+      const uint8_t* blk = sm + s * 2 * Q::BYTES;
+      int t0 = b * BT + warp * 16;                     // first of this warp's 16 tokens
+#pragma unroll 1
+      for (int u = 0; u < 2; ++u, blk += Q::BYTES, t0 += BT) {
+        if (((here >> u) & 1) == 0 || t0 >= walk.kv_len) continue;
         uint32_t ka[W], kb[W];
         lds_words<W>(ka, blk + (warp * 16 + g) * Q::KROW + j * (D / 8));
         lds_words<W>(kb, blk + (warp * 16 + g + 8) * Q::KROW + j * (D / 8));
