@@ -39,7 +39,7 @@ namespace {
 constexpr int AQ_WARPS = 4;                       // computing warps
 constexpr int AQ_THREADS = (AQ_WARPS + 1) * 32;   // + the producer
 constexpr int AQ_STAGES = 3;                      // of two slots each
-constexpr int AQ_MIN_STEPS = 2;                   // blocks that are worth a CTA of their own
+constexpr int AQ_MIN_STEPS = 4;                   // blocks that are worth a CTA of their own
 
 template <int D, int NT>
 struct AqSmem {
@@ -80,7 +80,7 @@ __device__ __forceinline__ void lds_words(uint32_t (&w)[N], const uint8_t* p) {
 
 // NT column groups of 8 query rows; SPLIT terms of q and p (1: bf16, 3: fp32)
 template <int D, int NT, int SPLIT>
-__global__ void __launch_bounds__(AQ_THREADS) attend_q4_kernel(const AttendQ4Params p) {
+__global__ void __launch_bounds__(AQ_THREADS, NT == 1 && SPLIT == 1 ? 3 : 2) attend_q4_kernel(const AttendQ4Params p) {
   using Q = Q4<D>;
   using SM = AqSmem<D, NT>;
   constexpr int ROWS = SM::ROWS, W = Q::WORDS;
@@ -232,9 +232,11 @@ __global__ void __launch_bounds__(AQ_THREADS) attend_q4_kernel(const AttendQ4Par
       const int here = meta[s];
       const uint8_t* blk = sm + s * 2 * Q::BYTES;
       int t0 = b * BT + warp * 16;                     // first of this warp's 16 tokens
-#pragma unroll 1
+      // both slots' instructions interleaved (one slot's chains do not fill the issue slots); a slot that is not
+      // there is masked
+#pragma unroll
       for (int u = 0; u < 2; ++u, blk += Q::BYTES, t0 += BT) {
-        if (((here >> u) & 1) == 0 || t0 >= walk.kv_len) continue;
+        const bool there = (here >> u) & 1;
         uint32_t ka[W], kb[W];
         lds_words<W>(ka, blk + (warp * 16 + g) * Q::KROW + j * (D / 8));
         lds_words<W>(kb, blk + (warp * 16 + g + 8) * Q::KROW + j * (D / 8));
@@ -284,16 +286,16 @@ __global__ void __launch_bounds__(AQ_THREADS) attend_q4_kernel(const AttendQ4Par
         }
         float sva = lo_bf16(vsa), svb = lo_bf16(vsb);
         float mva = fmaf(8.f, sva, hi_bf16(vsa)), mvb = fmaf(8.f, svb, hi_bf16(vsb));
-        const bool masked = t0 + 16 > lim_min;          // some column does not see all 16 tokens
+        const bool masked = !there || t0 + 16 > lim_min;          // some column does not see all 16 tokens
         if (masked) {
           // what lies behind the cached tokens was never written: its scales may be anything
-          if (t0 + g >= walk.kv_len) sva = mva = 0.f;
-          if (t0 + g + 8 >= walk.kv_len) svb = mvb = 0.f;
+          if (!there || t0 + g >= walk.kv_len) sva = mva = 0.f;
+          if (!there || t0 + g + 8 >= walk.kv_len) svb = mvb = 0.f;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              if (t0 + g + (i >> 1) * 8 >= lim[nt][i & 1]) x[nt][i] = -INFINITY;
+              if (!there || t0 + g + (i >> 1) * 8 >= lim[nt][i & 1]) x[nt][i] = -INFINITY;
         }
         bool grow = false;
 #pragma unroll

@@ -11,7 +11,7 @@ namespace pbsa {
 constexpr int Q4_MAX_CTAS = 640;      // of a grid of the few-rows kernel (16 rows a piece)
 constexpr int Q4_TC_MAX_CTAS = 160;   // of a grid of the tensor-core kernel (128 rows a piece)
 constexpr int Q4_PART_ROWS = 2 * (Q4_MAX_CTAS * 16 > Q4_TC_MAX_CTAS * 128 ? Q4_MAX_CTAS * 16 : Q4_TC_MAX_CTAS * 128);
-constexpr int Q4_TC_ROWS = 32;        // requests with more rows go to the tensor-core kernel
+constexpr int Q4_TC_ROWS = 48;        // requests with more rows go to the tensor-core kernel
 
 // A tile that starts in this CTA and ends in a later one (pieces = 0: none).
 struct __align__(8) Q4Desc {
@@ -41,6 +41,12 @@ struct AttendQ4Params {
   float* part_o;
   void* ws;
 };
+
+// a / b of non-negative numbers; 64-bit divisions are an order slower and rarely needed
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
 
 // sum over i in [0, n) of floor((a i + b) / m), for a, b >= 0, m > 0
 __device__ __forceinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
@@ -74,7 +80,7 @@ struct Q4Request {
     return n == 0 ? 0 : (long long)n * base + floor_sum(n, den, num, num + den - 1);
   }
   __device__ int charge(int mt) const {
-    return base < 0 ? blocks : base + (int)(((long long)num * (mt + 1) + den - 1) / den);
+    return base < 0 ? blocks : base + (int)quotient((long long)num * (mt + 1) + den - 1, den);
   }
   __device__ long long head_steps() const { return charged_to(tiles); }
 };
@@ -138,12 +144,15 @@ __device__ __forceinline__ Q4Share q4_share(const AttendQ4Params& p, int tile_ro
     if (w == warp) before = s.total;
     s.total += sums[w];
   }
-  const long long want = (s.total + min_steps - 1) / min_steps;
+  const long long want = quotient(s.total + min_steps - 1, min_steps);
   s.ctas = (int)(want < gridDim.x ? want : gridDim.x);
   s.x0 = s.x1 = 0;
   if ((int)blockIdx.x < s.ctas) {
-    s.x0 = s.total * blockIdx.x / s.ctas;
-    s.x1 = s.total * (blockIdx.x + 1) / s.ctas;
+    // floor(total i / ctas) of this CTA and the next
+    const long long whole = quotient(s.total, s.ctas);
+    const uint32_t rest = (uint32_t)(s.total - whole * s.ctas);
+    s.x0 = whole * blockIdx.x + rest * blockIdx.x / (uint32_t)s.ctas;
+    s.x1 = whole * (blockIdx.x + 1) + rest * (blockIdx.x + 1) / (uint32_t)s.ctas;
     long long at = before + upto - mine;
     if (s.x0 >= at && s.x0 < at + mine) {
       for (int r = r0; r < r1; ++r) {
@@ -183,7 +192,7 @@ struct Q4Walk {
     // the head and row tile of the share's first step
     req = q4_request(p, r, tile_rows, false);
     const long long head = req.head_steps();
-    h = (int)(s.off / head);
+    h = (int)quotient(s.off, head);
     const long long off = s.off - h * head;
     int lo = 0, hi = req.tiles - 1;
     while (lo < hi) {
@@ -229,7 +238,7 @@ struct Q4Walk {
       piece = 2 * blockIdx.x + 1;
       // the CTA that holds the tile's last step: the largest i with total * i / ctas <= that step
       const long long end_step = x + charge;
-      const int c1 = (int)((end_step * ctas + total - 1) / total) - 1;
+      const int c1 = (int)quotient(end_step * ctas + total - 1, total) - 1;
       desc.pieces = c1 - (int)blockIdx.x + 1;
       desc.row0 = mt * tile_rows;
       desc.rows = min(tile_rows, rows - desc.row0);
@@ -276,20 +285,37 @@ __global__ void __launch_bounds__(256) attend_q4_join_kernel(const AttendQ4Param
   const int ch = threadIdx.x % CH;
   auto at = [&](int k) { return (size_t)(k == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + k)) * p.part_rows; };
   for (int r = threadIdx.x / CH + RPP * blockIdx.y; r < d.rows; r += RPP * gridDim.y) {
-    float M = -INFINITY;
-#pragma unroll 8
-    for (int k = 0; k < d.pieces; ++k) M = fmaxf(M, p.part_ml[at(k) + r].x);
-    float L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-    for (int k = 0; k < d.pieces; ++k) {
-      const float2 ml = p.part_ml[at(k) + r];
-      const float4 v = *reinterpret_cast<const float4*>(p.part_o + (at(k) + r) * D + 4 * ch);
-      const float f = q4_weight(ml.x, M);
-      L = fmaf(f, ml.y, L);
-      acc[0] = fmaf(f, v.x, acc[0]);
-      acc[1] = fmaf(f, v.y, acc[1]);
-      acc[2] = fmaf(f, v.z, acc[2]);
-      acc[3] = fmaf(f, v.w, acc[3]);
+    // 8 pieces at a time, their loads in flight together (a place past the end repeats the last piece, unused)
+    float M = -INFINITY, L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int k0 = 0; k0 < d.pieces; k0 += 8) {
+      float2 ml[8];
+      float4 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const size_t place = at(min(k0 + i, d.pieces - 1)) + r;
+        ml[i] = p.part_ml[place];
+        v[i] = *reinterpret_cast<const float4*>(p.part_o + place * D + 4 * ch);
+      }
+      float top = M;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, ml[i].x);
+      const float f0 = M == top ? 1.f : q4_weight(M, top);
+      M = top;
+      L *= f0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] *= f0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (k0 + i < d.pieces) {
+          const float f = q4_weight(ml[i].x, M);
+          L = fmaf(f, ml[i].y, L);
+          acc[0] = fmaf(f, v[i].x, acc[0]);
+          acc[1] = fmaf(f, v[i].y, acc[1]);
+          acc[2] = fmaf(f, v[i].z, acc[2]);
+          acc[3] = fmaf(f, v[i].w, acc[3]);
+        }
+      }
     }
     q4_write_row<D>(p, d.q0, d.row0 + r, d.h, 4 * ch, acc, M, L, ch == 0);
   }

@@ -40,6 +40,7 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
 }
 
 constexpr int AP_THREADS = 256;
+constexpr int AP_UNROLL = 4;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(AP_THREADS) append_q4_kernel(const AppendParams p) {
@@ -50,58 +51,75 @@ __global__ void __launch_bounds__(AP_THREADS) append_q4_kernel(const AppendParam
   const int l = lane % LPV, part = (lane / LPV) & 1, sub = lane / (2 * LPV);
   const long long items = (long long)p.T * p.H;
   const long long warps = (long long)gridDim.x * (AP_THREADS / 32);
-  // every lane of a warp runs the same iterations (shuffles); items past the end are only not written
-  for (long long base = ((long long)blockIdx.x * (AP_THREADS / 32) + (threadIdx.x >> 5)) * PAIRS; base < items;
-       base += warps * PAIRS) {
-    const long long it = base + sub;
-    const bool in = it < items;
-    const int t = in ? (int)(it / p.H) : 0, h = in ? (int)(it - (long long)t * p.H) : 0;
-    const int at = in ? __ldg(p.slot_map + t) : -1;
-    const bool ok = at >= 0 && at < p.pool_slots * BT;
-    if (in && at != -1 && !ok && l == 0 && part == 0) record_error(p.ws, PBSA_ERR_DEVICE_INDEX, at, K_Q4_APPEND);
-    float x[8];
+  // AP_UNROLL items of a lane at once, so that their slots and then their values are in flight together.  Every
+  // lane of a warp runs the same iterations (shuffles); items past the end are only not written.
+  for (long long base = ((long long)blockIdx.x * (AP_THREADS / 32) + (threadIdx.x >> 5)) * (PAIRS * AP_UNROLL); base < items;
+       base += warps * (PAIRS * AP_UNROLL)) {
+    int at[AP_UNROLL], h[AP_UNROLL];
+    float x[AP_UNROLL][8];
+    long long src[AP_UNROLL];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = 0.f;
-    if (ok) load8(static_cast<const T*>(part ? p.v : p.k) + t * (part ? p.v_ld : p.k_ld) + (long long)h * D + 8 * l, x);
-    float lo = x[0], hi = x[0];
-#pragma unroll
-    for (int i = 1; i < 8; ++i) { lo = min_nan(lo, x[i]); hi = max_nan(hi, x[i]); }
-#pragma unroll
-    for (int o = 1; o < LPV; o <<= 1) {
-      lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-      hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    for (int u = 0; u < AP_UNROLL; ++u) {
+      const long long it = base + u * PAIRS + sub;
+      const bool in = it < items;
+      const int t = in ? (int)(it / p.H) : 0;
+      h[u] = in ? (int)(it - (long long)t * p.H) : 0;
+      at[u] = in ? __ldg(p.slot_map + t) : -1;
+      src[u] = t * (part ? p.v_ld : p.k_ld) + (long long)h[u] * D + 8 * l;
     }
-    float m = bf16_down(lo);
-    const float span = __fsub_rn(hi, m);
-    float s = bf16_up_pos(__fmul_rn(span, 1.0f / 15.0f));
-    s = span == 0.f ? 0.f : fmaxf(s, 1.17549435e-38f);
-    // (NaN compares false: fmaxf would drop it, so the operands are tested themselves)
-    const bool bad = !(fabsf(lo) < INFINITY && fabsf(hi) < INFINITY && fabsf(m) < INFINITY && s < INFINITY);
-    const unsigned votes = __ballot_sync(0xffffffffu, bad);
-    const unsigned pair = (2 * LPV == 32 ? 0xffffffffu : ((1u << (2 * LPV)) - 1u)) << (sub * 2 * LPV);
-    const bool poison = (votes & pair) != 0;
-    const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
-    uint32_t c[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      c[i] = poison ? 0u : min((uint32_t)__float2int_rn(__fmul_rn(__fsub_rn(x[i], m), inv)), 15u);
-    uint32_t sm = (__float_as_uint(s) >> 16) | (__float_as_uint(m) & 0xFFFF0000u);
-    if (poison) sm = part ? 0u : 0x7FC07FC0u;
-    if (!ok) continue;
-    const int slot = at / BT, row = at % BT;
-    uint8_t* blk = p.pool + ((size_t)h * p.pool_slots + slot) * Q::BYTES;
-    if (part == 0) {
-      uint32_t w = 0;
+    for (int u = 0; u < AP_UNROLL; ++u) {
+      const bool ok = at[u] >= 0 && at[u] < p.pool_slots * BT;
+      if (!ok && at[u] != -1) {
+        if (l == 0 && part == 0) record_error(p.ws, PBSA_ERR_DEVICE_INDEX, at[u], K_Q4_APPEND);
+        at[u] = -1;
+      }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w |= c[2 * i] << (4 * i) | c[2 * i + 1] << (4 * i + 16);
-      *reinterpret_cast<uint32_t*>(blk + row * Q::KROW + 4 * l) = w;
-      if (l == 0) *reinterpret_cast<uint32_t*>(blk + Q::OFF_KS + 4 * row) = sm;
-    } else {
-      // 8 channels are half words of words (8l % (D/8)) / 4 and the next of group 8l / (D/8)
-      uint8_t* dst = blk + Q::OFF_V + Q::v_at(row, (8 * l) / (D / 8)) + ((8 * l) % (D / 8));
-      *reinterpret_cast<uint16_t*>(dst) = (uint16_t)(c[0] | c[1] << 4 | c[2] << 8 | c[3] << 12);
-      *reinterpret_cast<uint16_t*>(dst + 4) = (uint16_t)(c[4] | c[5] << 4 | c[6] << 8 | c[7] << 12);
-      if (l == 0) *reinterpret_cast<uint32_t*>(blk + Q::OFF_VS + 4 * row) = sm;
+      for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
+      if (ok) load8(static_cast<const T*>(part ? p.v : p.k) + src[u], x[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < AP_UNROLL; ++u) {
+      float lo = x[u][0], hi = x[u][0];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) { lo = min_nan(lo, x[u][i]); hi = max_nan(hi, x[u][i]); }
+#pragma unroll
+      for (int o = 1; o < LPV; o <<= 1) {
+        lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+      }
+      const float m = bf16_down(lo);
+      const float span = __fsub_rn(hi, m);
+      float s = bf16_up_pos(__fmul_rn(span, 1.0f / 15.0f));
+      s = span == 0.f ? 0.f : fmaxf(s, 1.17549435e-38f);
+      // (NaN compares false: fmaxf would drop it, so the operands are tested themselves)
+      const bool bad = !(fabsf(lo) < INFINITY && fabsf(hi) < INFINITY && fabsf(m) < INFINITY && s < INFINITY);
+      const unsigned votes = __ballot_sync(0xffffffffu, bad);
+      const unsigned pair = (2 * LPV == 32 ? 0xffffffffu : ((1u << (2 * LPV)) - 1u)) << (sub * 2 * LPV);
+      const bool poison = (votes & pair) != 0;
+      const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
+      uint32_t c[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        c[i] = poison ? 0u : min((uint32_t)__float2int_rn(__fmul_rn(__fsub_rn(x[u][i], m), inv)), 15u);
+      uint32_t sm = (__float_as_uint(s) >> 16) | (__float_as_uint(m) & 0xFFFF0000u);
+      if (poison) sm = part ? 0u : 0x7FC07FC0u;
+      if (at[u] < 0) continue;
+      const int slot = at[u] / BT, row = at[u] % BT;
+      uint8_t* blk = p.pool + ((size_t)h[u] * p.pool_slots + slot) * Q::BYTES;
+      if (part == 0) {
+        uint32_t w = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w |= c[2 * i] << (4 * i) | c[2 * i + 1] << (4 * i + 16);
+        *reinterpret_cast<uint32_t*>(blk + row * Q::KROW + 4 * l) = w;
+        if (l == 0) *reinterpret_cast<uint32_t*>(blk + Q::OFF_KS + 4 * row) = sm;
+      } else {
+        // 8 channels are half words of words (8l % (D/8)) / 4 and the next of group 8l / (D/8)
+        uint8_t* dst = blk + Q::OFF_V + Q::v_at(row, (8 * l) / (D / 8)) + ((8 * l) % (D / 8));
+        *reinterpret_cast<uint16_t*>(dst) = (uint16_t)(c[0] | c[1] << 4 | c[2] << 8 | c[3] << 12);
+        *reinterpret_cast<uint16_t*>(dst + 4) = (uint16_t)(c[4] | c[5] << 4 | c[6] << 8 | c[7] << 12);
+        if (l == 0) *reinterpret_cast<uint32_t*>(blk + Q::OFF_VS + 4 * row) = sm;
+      }
     }
   }
 }
@@ -175,7 +193,8 @@ __global__ void __launch_bounds__(EX_THREADS) expand_q4_kernel(const ExpandParam
 
 template <typename T, int D>
 cudaError_t append_t(const AppendParams& p, cudaStream_t st) {
-  const long long warps = ((long long)p.T * p.H + (32 / (D / 4)) - 1) / (32 / (D / 4));
+  constexpr int PER_WARP = 32 / (D / 4) * AP_UNROLL;
+  const long long warps = ((long long)p.T * p.H + PER_WARP - 1) / PER_WARP;
   const long long ctas = (warps + AP_THREADS / 32 - 1) / (AP_THREADS / 32);
   append_q4_kernel<T, D><<<(unsigned)(ctas < 148 * 8 ? ctas : 148 * 8), AP_THREADS, 0, st>>>(p);
   return cudaGetLastError();

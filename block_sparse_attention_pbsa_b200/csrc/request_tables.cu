@@ -10,11 +10,11 @@
 // prefix sums of all requests for itself (a few hundred cycles) and then does its share of the
 // maps: no CTA waits for another's results.
 //
-// The in-place state (lengths, the free count) may be the same memory as the outputs: one cluster
-// holds all CTAs, and the outputs that may alias inputs are written after a cluster barrier that
-// every CTA reaches with those inputs in its shared memory.  Table rows and the free stack need no
-// barrier: a call reads table entries below blocks(len_r) and stack entries below the free count,
-// and writes only entries at or above them.
+// Where the state (lengths, the free count) is kept in place, outputs are the same memory as inputs: one
+// cluster then holds all CTAs, and those outputs are written after a cluster barrier that every CTA
+// reaches with the inputs in its shared memory.  With outputs apart, as many CTAs as the rows fill start
+// without one.  Table rows and the free stack need no barrier: a call reads table entries below
+// blocks(len_r) and stack entries below the free count, and writes only entries at or above them.
 //
 // Bound by latency (the sums, a binary search per token, one dependent table read), not bytes.
 #include "common.cuh"
@@ -25,6 +25,7 @@ namespace {
 
 constexpr int RT_THREADS = 1024;
 constexpr int RT_CLUSTER = 8;
+constexpr int RT_MAX_CTAS = 148;
 
 struct TablesParams {
   const int* step_len;
@@ -38,6 +39,7 @@ struct TablesParams {
   int T;
   int *q_start, *q_len, *kv_len, *free_cnt_out, *slot_map, *position;
   void* ws;
+  int in_place;   // kv_len or free_cnt_out may share memory with an input
 };
 
 // Inclusive block sums of two values per thread (all threads call it).
@@ -90,9 +92,7 @@ __global__ void __launch_bounds__(RT_THREADS) request_tables_kernel(const Tables
   const int tid = threadIdx.x;
   const int per = (p.R + RT_THREADS - 1) / RT_THREADS;
   const int r0 = min(tid * per, p.R), r1 = min(r0 + per, p.R);
-  uint32_t nctas, rank;
-  asm("mov.u32 %0, %cluster_nctaid.x;" : "=r"(nctas));
-  asm("mov.u32 %0, %cluster_ctarank;" : "=r"(rank));
+  const int nctas = gridDim.x, rank = blockIdx.x;   // in place, the grid is one cluster
 
   int cnt = *p.free_cnt;
   if (cnt < 0 || cnt > p.pool_slots) {
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(RT_THREADS) request_tables_kernel(const Tables
   }
   __syncthreads();
   // the inputs that an output may share memory with have been read by this CTA
-  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+  if (p.in_place) asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 
   const int taken = s_taken;
   const long long left_all = avail - taken;
@@ -209,13 +209,21 @@ __global__ void __launch_bounds__(RT_THREADS) request_tables_kernel(const Tables
 cudaError_t launch_request_tables(const int* step_len, const int* seq_len, int R, int* table, int ld, int* free_slot,
                                   const int* free_cnt, int pool_slots, int T, int* q_start, int* q_len, int* kv_len,
                                   int* free_cnt_out, int* slot_map, int* position, void* ws, cudaStream_t st) {
+  // (compared as ranges: the outputs may also overlap an input in part)
+  auto overlap = [](const int* a, int na, const int* b, int nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + sizeof(int) * (size_t)nb && y < x + sizeof(int) * (size_t)na;
+  };
+  const int in_place = overlap(kv_len, R, seq_len, R) || overlap(free_cnt_out, 1, free_cnt, 1) ||
+                       overlap(kv_len, R, step_len, R) || overlap(q_len, R, step_len, R) || overlap(q_len, R, seq_len, R);
   const TablesParams p = {step_len, seq_len, R,      table, ld,           free_slot, free_cnt, pool_slots,
-                          T,        q_start, q_len, kv_len, free_cnt_out, slot_map,  position, ws};
+                          T,        q_start, q_len, kv_len, free_cnt_out, slot_map,  position, ws, in_place};
   const int smem = 5 * R * (int)sizeof(int);
   cudaError_t e = set_smem_once((const void*)request_tables_kernel, 5 * 8192 * (int)sizeof(int));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  const int ctas = T <= RT_THREADS ? 1 : RT_CLUSTER;
+  const int fill = (T + RT_THREADS - 1) / RT_THREADS;
+  const int ctas = fill <= 1 ? 1 : in_place ? RT_CLUSTER : (fill < RT_MAX_CTAS ? fill : RT_MAX_CTAS);
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(RT_THREADS);
   cfg.dynamicSmemBytes = smem;
@@ -226,7 +234,7 @@ cudaError_t launch_request_tables(const int* step_len, const int* seq_len, int R
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = in_place ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, request_tables_kernel, p);
 }
 
