@@ -27,67 +27,113 @@ struct AppendParams {
   void* ws;
 };
 
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+// 8 neighbouring channels as they lie in memory.
+template <typename T>
+struct Eight;
+template <>
+struct Eight<float> {
+  float4 a, b;
+  __device__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ void load(const float* p) {
+    a = __ldg(reinterpret_cast<const float4*>(p));
+    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ void values(float (&x)[8]) const {
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  }
+  // least and greatest of the vector that `N` neighbouring threads hold (NaN if any is)
+  template <int N>
+  __device__ void range(float& lo, float& hi) const {
+    float x[8];
+    values(x);
+    lo = hi = x[0];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) { x[2 * i] = lo_bf16(w[i]); x[2 * i + 1] = hi_bf16(w[i]); }
+    for (int i = 1; i < 8; ++i) { lo = min_nan(lo, x[i]); hi = max_nan(hi, x[i]); }
+#pragma unroll
+    for (int o = 1; o < N; o <<= 1) {
+      lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+  }
+};
+__device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+template <>
+struct Eight<__nv_bfloat16> {
+  uint4 a;
+  __device__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ void load(const __nv_bfloat16* p) { a = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ void values(float (&x)[8]) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { x[2 * i] = lo_bf16(w[i]); x[2 * i + 1] = hi_bf16(w[i]); }
+  }
+  // as above, two at a time: (least, -greatest) travel as one pair of bf16, both taken by minima
+  template <int N>
+  __device__ void range(float& lo, float& hi) const {
+    const uint32_t least = min2_nan(min2_nan(a.x, a.y), min2_nan(a.z, a.w)), n = 0x80008000u;
+    const uint32_t most = min2_nan(min2_nan(a.x ^ n, a.y ^ n), min2_nan(a.z ^ n, a.w ^ n));
+    uint32_t r = min2_nan(__byte_perm(least, most, 0x5410), __byte_perm(least, most, 0x7632));
+#pragma unroll
+    for (int o = 1; o < N; o <<= 1) r = min2_nan(r, __shfl_xor_sync(0xffffffffu, r, o));
+    lo = lo_bf16(r);
+    hi = -hi_bf16(r);
+  }
+};
+
+// round(x) in the low bits of the result, which carries a constant above them (0 <= x < 2^21, ties to even)
+__device__ __forceinline__ uint32_t rounded_bits(float x) { return __float_as_uint(__fadd_rn(x, 12582912.f)); }
+// four codes as nibbles: multiply-adds on the rounded floats' bits, the constant taken off at the end
+__device__ __forceinline__ uint32_t four(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return a + 16u * b + 256u * c + 4096u * d - 4369u * 0x4B400000u;
 }
 
 constexpr int AP_THREADS = 256;
-constexpr int AP_UNROLL = 4;
 
-template <typename T, int D>
+// U neighbouring tokens of a head at once: their slots and then their values are in flight together, and the two
+// tokens that share V's words are mostly written as one
+template <typename T, int D, int U>
 __global__ void __launch_bounds__(AP_THREADS) append_q4_kernel(const AppendParams p) {
   constexpr int LPV = D / 8;            // threads of a vector
   constexpr int PAIRS = 32 / (2 * LPV);  // (token, head) pairs of a warp
   using Q = Q4<D>;
   const int lane = threadIdx.x & 31;
   const int l = lane % LPV, part = (lane / LPV) & 1, sub = lane / (2 * LPV);
-  const long long items = (long long)p.T * p.H;
+  const int runs = (p.T + U - 1) / U;                 // of U neighbouring tokens
+  const long long items = (long long)runs * p.H;
   const long long warps = (long long)gridDim.x * (AP_THREADS / 32);
-  // AP_UNROLL items of a lane at once, so that their slots and then their values are in flight together.  Every
-  // lane of a warp runs the same iterations (shuffles); items past the end are only not written.
-  for (long long base = ((long long)blockIdx.x * (AP_THREADS / 32) + (threadIdx.x >> 5)) * (PAIRS * AP_UNROLL); base < items;
-       base += warps * (PAIRS * AP_UNROLL)) {
-    int at[AP_UNROLL], h[AP_UNROLL];
-    float x[AP_UNROLL][8];
-    long long src[AP_UNROLL];
+  // every lane of a warp runs the same iterations (shuffles); items past the end are only not written
+  for (long long base = ((long long)blockIdx.x * (AP_THREADS / 32) + (threadIdx.x >> 5)) * PAIRS; base < items;
+       base += warps * PAIRS) {
+    const long long it = base + sub;
+    const bool in = it < items;
+    const int run = in ? (int)(it / p.H) : 0, h = in ? (int)(it - (long long)run * p.H) : 0;
+    int at[U];
+    Eight<T> x[U];
 #pragma unroll
-    for (int u = 0; u < AP_UNROLL; ++u) {
-      const long long it = base + u * PAIRS + sub;
-      const bool in = it < items;
-      const int t = in ? (int)(it / p.H) : 0;
-      h[u] = in ? (int)(it - (long long)t * p.H) : 0;
-      at[u] = in ? __ldg(p.slot_map + t) : -1;
-      src[u] = t * (part ? p.v_ld : p.k_ld) + (long long)h[u] * D + 8 * l;
-    }
+    for (int u = 0; u < U; ++u) at[u] = in && run * U + u < p.T ? __ldg(p.slot_map + run * U + u) : -1;
+    const T* src = static_cast<const T*>(part ? p.v : p.k) + (long long)run * U * (part ? p.v_ld : p.k_ld) + (long long)h * D + 8 * l;
 #pragma unroll
-    for (int u = 0; u < AP_UNROLL; ++u) {
+    for (int u = 0; u < U; ++u) {
       const bool ok = at[u] >= 0 && at[u] < p.pool_slots * BT;
       if (!ok && at[u] != -1) {
         if (l == 0 && part == 0) record_error(p.ws, PBSA_ERR_DEVICE_INDEX, at[u], K_Q4_APPEND);
         at[u] = -1;
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
-      if (ok) load8(static_cast<const T*>(part ? p.v : p.k) + src[u], x[u]);
+      x[u].zero();
+      if (ok) x[u].load(src + u * (part ? p.v_ld : p.k_ld));
     }
+    uint32_t lower[U], upper[U];   // K: a word's even and odd channels; V: channels 0 .. 3 and 4 .. 7
+    uint32_t sm[U];
 #pragma unroll
-    for (int u = 0; u < AP_UNROLL; ++u) {
-      float lo = x[u][0], hi = x[u][0];
-#pragma unroll
-      for (int i = 1; i < 8; ++i) { lo = min_nan(lo, x[u][i]); hi = max_nan(hi, x[u][i]); }
-#pragma unroll
-      for (int o = 1; o < LPV; o <<= 1) {
-        lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-      }
+    for (int u = 0; u < U; ++u) {
+      float lo, hi, v[8];
+      x[u].template range<LPV>(lo, hi);
+      x[u].values(v);
       const float m = bf16_down(lo);
       const float span = __fsub_rn(hi, m);
       float s = bf16_up_pos(__fmul_rn(span, 1.0f / 15.0f));
@@ -98,27 +144,37 @@ __global__ void __launch_bounds__(AP_THREADS) append_q4_kernel(const AppendParam
       const unsigned pair = (2 * LPV == 32 ? 0xffffffffu : ((1u << (2 * LPV)) - 1u)) << (sub * 2 * LPV);
       const bool poison = (votes & pair) != 0;
       const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
+      // no code is above 15: s >= (hi - m) / 15 (1 - 2^-23), and 15.5 is far off
       uint32_t c[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        c[i] = poison ? 0u : min((uint32_t)__float2int_rn(__fmul_rn(__fsub_rn(x[u][i], m), inv)), 15u);
-      uint32_t sm = (__float_as_uint(s) >> 16) | (__float_as_uint(m) & 0xFFFF0000u);
-      if (poison) sm = part ? 0u : 0x7FC07FC0u;
+      for (int i = 0; i < 8; ++i) c[i] = rounded_bits(__fmul_rn(__fsub_rn(v[i], m), inv));
+      lower[u] = part ? four(c[0], c[1], c[2], c[3]) : four(c[0], c[2], c[4], c[6]);
+      upper[u] = part ? four(c[4], c[5], c[6], c[7]) : four(c[1], c[3], c[5], c[7]);
+      sm[u] = (__float_as_uint(s) >> 16) | (__float_as_uint(m) & 0xFFFF0000u);
+      if (poison) {
+        lower[u] = upper[u] = 0u;
+        sm[u] = part ? 0u : 0x7FC07FC0u;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
       if (at[u] < 0) continue;
       const int slot = at[u] / BT, row = at[u] % BT;
-      uint8_t* blk = p.pool + ((size_t)h[u] * p.pool_slots + slot) * Q::BYTES;
+      uint8_t* blk = p.pool + ((size_t)h * p.pool_slots + slot) * Q::BYTES;
+      if (l == 0) *reinterpret_cast<uint32_t*>(blk + (part ? Q::OFF_VS : Q::OFF_KS) + 4 * row) = sm[u];
       if (part == 0) {
-        uint32_t w = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w |= c[2 * i] << (4 * i) | c[2 * i + 1] << (4 * i + 16);
-        *reinterpret_cast<uint32_t*>(blk + row * Q::KROW + 4 * l) = w;
-        if (l == 0) *reinterpret_cast<uint32_t*>(blk + Q::OFF_KS + 4 * row) = sm;
-      } else {
-        // 8 channels are half words of words (8l % (D/8)) / 4 and the next of group 8l / (D/8)
-        uint8_t* dst = blk + Q::OFF_V + Q::v_at(row, (8 * l) / (D / 8)) + ((8 * l) % (D / 8));
-        *reinterpret_cast<uint16_t*>(dst) = (uint16_t)(c[0] | c[1] << 4 | c[2] << 8 | c[3] << 12);
-        *reinterpret_cast<uint16_t*>(dst + 4) = (uint16_t)(c[4] | c[5] << 4 | c[6] << 8 | c[7] << 12);
-        if (l == 0) *reinterpret_cast<uint32_t*>(blk + Q::OFF_VS + 4 * row) = sm;
+        *reinterpret_cast<uint32_t*>(blk + row * Q::KROW + 4 * l) = lower[u] | upper[u] << 16;
+        continue;
+      }
+      // 8 channels are half words of words (8l % (D/8)) / 4 and the next of group 8l / (D/8); the two tokens of a word
+      // are written together where both are here
+      uint8_t* dst = blk + Q::OFF_V + Q::v_at(row, (8 * l) / (D / 8)) + ((8 * l) % (D / 8));
+      if (u + 1 < U && (row & 1) == 0 && at[u + 1 < U ? u + 1 : u] == at[u] + 1) {
+        *reinterpret_cast<uint32_t*>(dst) = lower[u] | lower[u + 1 < U ? u + 1 : u] << 16;
+        *reinterpret_cast<uint32_t*>(dst + 4) = upper[u] | upper[u + 1 < U ? u + 1 : u] << 16;
+      } else if (u == 0 || (row & 1) == 0 || at[u > 0 ? u - 1 : 0] != at[u] - 1) {
+        *reinterpret_cast<uint16_t*>(dst) = (uint16_t)lower[u];
+        *reinterpret_cast<uint16_t*>(dst + 4) = (uint16_t)upper[u];
       }
     }
   }
@@ -191,13 +247,19 @@ __global__ void __launch_bounds__(EX_THREADS) expand_q4_kernel(const ExpandParam
   }
 }
 
+template <typename T, int D, int U>
+cudaError_t append_u(const AppendParams& p, cudaStream_t st) {
+  constexpr int PAIRS = 32 / (D / 4);
+  const long long warps = ((long long)((p.T + U - 1) / U) * p.H + PAIRS - 1) / PAIRS;
+  const long long ctas = (warps + AP_THREADS / 32 - 1) / (AP_THREADS / 32);
+  append_q4_kernel<T, D, U><<<(unsigned)(ctas < 148 * 8 ? ctas : 148 * 8), AP_THREADS, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
 template <typename T, int D>
 cudaError_t append_t(const AppendParams& p, cudaStream_t st) {
-  constexpr int PER_WARP = 32 / (D / 4) * AP_UNROLL;
-  const long long warps = ((long long)p.T * p.H + PER_WARP - 1) / PER_WARP;
-  const long long ctas = (warps + AP_THREADS / 32 - 1) / (AP_THREADS / 32);
-  append_q4_kernel<T, D><<<(unsigned)(ctas < 148 * 8 ? ctas : 148 * 8), AP_THREADS, 0, st>>>(p);
-  return cudaGetLastError();
+  // a few items are spread over warps, many are loaded four at a time
+  return (long long)p.T * p.H < 16384 ? append_u<T, D, 1>(p, st) : append_u<T, D, 4>(p, st);
 }
 
 }  // namespace
