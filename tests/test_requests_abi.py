@@ -96,3 +96,24 @@ def test_binding_refuses_host_tensors():
     with pytest.raises((ValueError, RuntimeError, AssertionError)):
         P.pbsa_append_q4(g, torch.zeros(4, 2, 64, dtype=torch.bfloat16), torch.zeros(4, 2, 64, dtype=torch.bfloat16), i,
                          torch.zeros(2 * 3 * 4608, dtype=torch.uint8), 3)
+
+
+def test_batch_refusals_on_the_host():
+    """Checks of serve.RequestBatch that come before any device work (a batch on the CPU: nothing is launched)."""
+    b = P.RequestBatch(P.RequestConfig(requests=2, blocks=2, tokens=10, pool_slots=3), device="cpu")
+    with pytest.raises(ValueError):
+        b.step([1, 1], 11)               # more than the rows
+    with pytest.raises(ValueError):
+        b.step([5, 1], 4)                # an entry above the bound
+    with pytest.raises(ValueError):
+        b.step([1, 1, 1], 4)             # another number of requests
+    with pytest.raises(ValueError):
+        P.Q4LayerCache(b, 3, 2, 128)     # heads that do not divide
+    with pytest.raises(ValueError):
+        P.Q4LayerCache(b, 2, 2, 96)
+    c = P.Q4LayerCache(b, 2, 2, 64)
+    assert c.kv_bytes == 2 * 3 * 4608
+    with pytest.raises(ValueError):
+        c.append(torch.zeros(9, 2, 64), torch.zeros(9, 2, 64))
+    with pytest.raises(ValueError):
+        c.attend(torch.zeros(9, 2, 64))
