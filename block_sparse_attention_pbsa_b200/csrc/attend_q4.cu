@@ -64,8 +64,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-// x - (the bf16 nearest x): what the next term of a split holds
-__device__ __forceinline__ float bf16_rest(float x) { return x - __bfloat162float(__float2bfloat16_rn(x)); }
 
 template <int N>
 __device__ __forceinline__ void lds_words(uint32_t (&w)[N], const uint8_t* p) {

@@ -9,9 +9,12 @@
 //  * Each step covers two blocks (128 keys).  Warp 0 brings the slots' bytes into a ring with bulk copies;
 //    two warpgroups, alternate steps, unpack them into shared-memory operand tiles (128-byte swizzle): K as
 //    the codes themselves (plus 128, exact in bf16), V as bf16 values s*c + m, rounded once, the bits that
-//    pbsa_expand_q4 gives.  The scores then get their scale and minimum in fp32, per key:
-//      x = s (q . (c + 128)) + (m - 128 s) sum(q),
-//    so they carry no rounding of K; rounding K to bf16 would put 2^-8 |q . k| / sqrt(d) of noise into each.
+//    pbsa_expand_q4 gives.  The scores carry no rounding of K (to bf16 it would put 2^-8 |q . k| / sqrt(d) of
+//    noise into each):
+//      q . k = s (q . (c + 128) + (m / s - 128) sum(q)).
+//    The bracket is one product: (m / s - 128) and sum(q) as three bf16 terms each make a further slice of 16
+//    columns of K and Q.  The scale is applied to the scores in fp32; the softmax reads it as bf16, eight
+//    keys a load, since what every lane of a warp reads from shared memory costs as much as distinct data.
 //  * TMEM: two S, two P (bf16) and one O (512 columns at D = 128); two softmax warpgroups on alternate steps, two
 //    MMA-issuing threads, one for each.  QK(i+2) is issued as soon as S(i) has been read, ahead of PV(i).
 //    The softmax makes one pass over a step's scores: scale, exponential, sum and maximum together, against
@@ -36,11 +39,12 @@ namespace {
 
 constexpr int TQ_THREADS = 640;      // warpgroups: control, unpack x 2, softmax x 2
 constexpr int TQ_MIN_STEPS = 8;      // blocks that are worth a CTA of their own
-constexpr int CST = 3, KST = 2, VST = 2, SCS = 4;
+constexpr int KCST = 3, VCST = 2, KST = 2, VST = 2, SCS = 4;   // code rings, operand stages, key scales
 constexpr uint32_t REG_CTRL = 48, REG_UNPACK = 80, REG_SOFT = 136;   // launched with 96: 48 + 2*80 + 2*136 = 5*96
 static_assert(REG_CTRL + 2 * REG_UNPACK + 2 * REG_SOFT <= 5 * 96, "register split exceeds the launch");
 
-enum { T_QFULL = 0, T_CFULL = 1, T_CEMPTY = T_CFULL + 2 * CST, T_KFULL = T_CEMPTY + 2 * CST,   // codes: K ring, V ring
+enum { T_QFULL = 0, T_CFULL = 1, T_CEMPTY = T_CFULL + KCST + VCST,   // codes: K ring, then V ring
+       T_KFULL = T_CEMPTY + KCST + VCST,
        T_KEMPTY = T_KFULL + KST,
        T_VFULL = T_KEMPTY + KST, T_VEMPTY = T_VFULL + VST, T_SCFULL = T_VEMPTY + VST, T_SFULL = T_SCFULL + SCS,
        T_PFULL = T_SFULL + 2, T_PVDONE = T_PFULL + 2, T_MMADONE = T_PVDONE + 2, T_XDONE = T_MMADONE + 1,
@@ -60,18 +64,19 @@ struct TqSmem {
   static constexpr uint32_t Q = 0;
   static constexpr uint32_t K = TILE;
   static constexpr uint32_t V = K + KST * TILE;
-  static constexpr uint32_t CODES = V + VST * TILE;
-  static constexpr uint32_t SC = CODES + 2 * CST * STEP;            // (the ring of K codes, then that of V codes;) float
-                                                                    // [SCS][2][128]: per key, scale and offset
-  static constexpr uint32_t QS = SC + SCS * 1024;                   // float [2][128]: sums of the halves of Q's rows
-  static constexpr uint32_t MREF = QS + 1024;                       // float2 [128]
+  static constexpr uint32_t QX = V + VST * TILE;                    // 16 more columns of Q: [16 groups of 8 rows][2][8][8]
+  static constexpr uint32_t KX = QX + 4096;                         // ... and of each K stage
+  static constexpr uint32_t CODES = KX + KST * 4096;                // the ring of K codes, then that of V codes
+  static constexpr uint32_t SC = CODES + (KCST + VCST) * STEP;      // bf16 [SCS][128]: scales of the step's keys
+  static constexpr uint32_t QS = SC + SCS * 256;                    // float [128]: sums of a half of Q's rows
+  static constexpr uint32_t MREF = QS + 512;                       // float2 [128]
   static constexpr uint32_t RLAST = MREF + 1024;                    // float [128]
   static constexpr uint32_t STAT = RLAST + 512;                     // float2 [2][128]
-  static constexpr uint32_t IDENT = STAT + 2048;                    // float [2][128]: a scale of 1, an offset of 0
-  static constexpr uint32_t BARS = IDENT + 1024;
+  static constexpr uint32_t ONES = STAT + 2048;                     // bf16 [128]: scales of scores that have theirs
+  static constexpr uint32_t BARS = ONES + 256;
   static constexpr uint32_t WALK = BARS + T_BARS * 8;               // TqPiece [2]
-  static constexpr uint32_t META = WALK + 2 * sizeof(TqPiece);      // int [2 CST][2], int [SCS], TMEM address, abort flag
-  static constexpr uint32_t TOTAL = META + 4 * (4 * CST + SCS + 2);
+  static constexpr uint32_t META = WALK + 2 * sizeof(TqPiece);      // int [rings][2], int [SCS], TMEM address, abort flag
+  static constexpr uint32_t TOTAL = META + 4 * (2 * (KCST + VCST) + SCS + 2);
   static constexpr uint32_t BYTES = TOTAL + 1024;
 };
 static_assert(TqSmem<128>::BYTES <= 232448, "shared memory");
@@ -92,6 +97,11 @@ __device__ __forceinline__ f32x2 fma2(f32x2 x, f32x2 y, f32x2 z) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
   return d;
 }
+__device__ __forceinline__ f32x2 mul2(f32x2 x, f32x2 y) {
+  f32x2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+  return d;
+}
 __device__ __forceinline__ f32x2 add2(f32x2 x, f32x2 y) {
   f32x2 d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
@@ -108,6 +118,13 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
   return r;
 }
 
+// Shared-memory matrix descriptor of 16 columns without swizzle: 8 x 8 blocks of 128 bytes, 128 bytes apart along
+// the columns, 256 along the rows (QX, KX).
+__device__ __forceinline__ uint64_t plain_desc(uint32_t smem_addr) {
+  return (uint64_t)((smem_addr & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 16 | (uint64_t)(256 >> 4) << 32 | (uint64_t)1 << 46;
+}
+__device__ __forceinline__ uint32_t plain_row(int row) { return (row >> 3) * 256 + (row & 7) * 16; }
+
 template <int D>
 __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const AttendQ4Params p) {
   using Q = Q4<D>;
@@ -115,10 +132,10 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + SM::BARS);
-  volatile int* meta = reinterpret_cast<volatile int*>(sm + SM::META);          // [2 CST][2]: the block is there
-  volatile int* sc_ok = meta + 4 * CST;                                         // [SCS]: the same, two bits
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + SM::META) + 4 * CST + SCS;
-  volatile int* abort_flag = meta + 4 * CST + SCS + 1;
+  volatile int* meta = reinterpret_cast<volatile int*>(sm + SM::META);          // [KCST + VCST][2]: the block is there
+  volatile int* sc_ok = meta + 2 * (KCST + VCST);                                         // [SCS]: the same, two bits
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + SM::META) + 2 * (KCST + VCST) + SCS;
+  volatile int* abort_flag = meta + 2 * (KCST + VCST) + SCS + 1;
   __shared__ Q4Start start_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -131,7 +148,10 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (tid < 256) reinterpret_cast<float*>(sm + SM::IDENT)[tid] = tid < 128 ? 1.f : 0.f;
+  if (tid < 64) reinterpret_cast<uint32_t*>(sm + SM::ONES)[tid] = 0x3F803F80u;
+  // the columns behind the six that are written stay zero
+  for (int i = tid; i < (1 + KST) * 1024; i += TQ_THREADS) reinterpret_cast<uint32_t*>(sm + SM::QX)[i] = 0u;
+  fence_proxy_async_smem();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == 1) {
     tmem_alloc(tmem_holder, 512);
@@ -192,8 +212,8 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
             const bool has1 = b + 1 < walk.b1;
             if (b + 2 < walk.b1) next0 = __ldg(row + b + 2);
             if (b + 3 < walk.b1) next1 = __ldg(row + b + 3);
-            const int cs = lane * CST + n % CST;
-            wait(T_CEMPTY + cs, ((n / CST) & 1) ^ 1);
+            const int depth = lane ? VCST : KCST, cs = lane * KCST + n % depth;
+            wait(T_CEMPTY + cs, ((n / depth) & 1) ^ 1);
             if (*abort_flag) break;
             const bool ok0 = slot0 >= 0 && slot0 < p.pool_slots, ok1 = has1 && slot1 >= 0 && slot1 < p.pool_slots;
             if (!ok0) record_error(p.ws, PBSA_ERR_DEVICE_INDEX, slot0, K_Q4_ATTEND);
@@ -212,9 +232,11 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
         __syncwarp();
       }
       // the CTA must not end with copies in flight
-      if (lane < 2)
-        for (int i = max(0, n - CST); i < n; ++i)
-          mbar_wait(&bars[T_CFULL + lane * CST + i % CST], (i / CST) & 1, kWaitLimitNs);
+      if (lane < 2) {
+        const int depth = lane ? VCST : KCST;
+        for (int i = max(0, n - depth); i < n; ++i)
+          mbar_wait(&bars[T_CFULL + lane * KCST + i % depth], (i / depth) & 1, kWaitLimitNs);
+      }
       __syncwarp();
     }
     if (warp == 1 || warp == 3) {
@@ -225,6 +247,7 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
         const uint64_t dq = sw128_desc(smem_u32(sm + SM::Q), 16, 1024);
         const uint64_t dk = sw128_desc(smem_u32(sm + SM::K), 16, 1024);
         const uint64_t dv = sw128_desc(smem_u32(sm + SM::V), 16384, 1024);
+        const uint64_t dqx = plain_desc(smem_u32(sm + SM::QX)), dkx = plain_desc(smem_u32(sm + SM::KX));
         constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, 128, 0, 0), IDESC_PV = idesc_bf16_f32(128, D, 0, 1);
         auto issue_qk = [&](int n) {
           const int sk = n % KST;
@@ -236,6 +259,7 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
             const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
             mma_bf16_ss(tmem + w * 128, dq + off, dk + ((sk * SM::TILE) >> 4) + off, IDESC_QK, kk > 0 ? 1u : 0u);
           }
+          mma_bf16_ss(tmem + w * 128, dqx, dkx + ((sk * 4096) >> 4), IDESC_QK, 1u);
           mma_commit(&bars[T_SFULL + w]);
           mma_commit(&bars[T_KEMPTY + sk]);
         };
@@ -303,14 +327,23 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
           for (int i = 0; i < 4; ++i) sum += lo_bf16(u[i]) + hi_bf16(u[i]);
           *reinterpret_cast<uint4*>(sm + SM::Q + (c >> 3) * 16384 + t * 128 + (((c & 7) ^ (t & 7)) << 4)) = v;
         }
-        reinterpret_cast<float*>(sm + SM::QS)[ug * 128 + t] = sum;
+        // the row's sum as three bf16 terms, beside which a key has three of its offset: columns
+        // (1, 2, 3, 1, 2, 1) of the one against (1, 1, 1, 2, 2, 3) of the other
+        if (ug == 1) reinterpret_cast<float*>(sm + SM::QS)[t] = sum;
+        asm volatile("bar.sync 2, 256;" ::: "memory");
+        if (ug == 0) {
+          sum += reinterpret_cast<const float*>(sm + SM::QS)[t];
+          const float s2 = bf16_rest(sum), s3 = bf16_rest(s2);
+          *reinterpret_cast<uint4*>(sm + SM::QX + plain_row(t)) =
+              make_uint4(pack_bf16(sum, s2), pack_bf16(s3, sum), pack_bf16(s2, sum), 0u);
+        }
         fence_proxy_async_smem();
         mbar_arrive(&bars[T_QFULL]);
       }
       const int n1 = n + ((walk.b1 - walk.b0 + 1) >> 1), start = n, first = n + ((n ^ ug) & 1);
       auto unpack_k = [&](int n) {
-        const int cs = n % CST, sk = n % KST;
-        wait(T_CFULL + cs, (n / CST) & 1);
+        const int cs = n % KCST, sk = n % KST;
+        wait(T_CFULL + cs, (n / KCST) & 1);
         const uint8_t* codes = sm + SM::CODES + cs * SM::STEP;
         // K: 16 (D = 64: 8) code bytes a lane; 8 lanes write 4 rows of two neighbouring column groups, 8
         // different 16-byte columns after the swizzle.  All of a thread's codes are read before the first is used.
@@ -332,12 +365,18 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
           }
           uint8_t* dst = sm + SM::K + sk * SM::TILE + ((j * W) >> 3) * 16384 + row0 * 128;
           wait(T_KEMPTY + sk, ((n / KST) & 1) ^ 1);   // QK(n-2) is done, and before it the softmax of step n-4
-          {   // scale and offset of key t, in log2 units
+          {   // key t: its scale, and what the sum of the row is multiplied by (see the top of the file)
             const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + (t >> 6) * Q::HALF + Q::OFF_KS + (t & 63) * 4);
-            float* sc = reinterpret_cast<float*>(sm + SM::SC) + (n % SCS) * 256;
-            const float s = lo_bf16(w);
-            sc[t] = s * p.scale_log2;
-            sc[128 + t] = fmaf(-128.f, s, hi_bf16(w)) * p.scale_log2;
+            const float m = hi_bf16(w);
+            float s = lo_bf16(w);
+            // a scale that is nothing beside the minimum (0: all channels are m): the minimum alone, scaled by itself
+            if (s <= fabsf(m) * 0x1p-60f) s = m == 0.f ? 1.f : fabsf(m);
+            const float r = __fdiv_rn(m, s) - 128.f;
+            const float r2 = bf16_rest(r), r3 = bf16_rest(r2);
+            const uint32_t r11 = pack_bf16(r, r);
+            *reinterpret_cast<uint4*>(sm + SM::KX + sk * 4096 + plain_row(t)) =
+                make_uint4(r11, pack_bf16(r, r2), pack_bf16(r2, r3), 0u);
+            reinterpret_cast<uint16_t*>(sm + SM::SC)[(n % SCS) * 128 + t] = (uint16_t)(__float_as_uint(s) >> 16);
             if (t == 0) sc_ok[n % SCS] = (meta[2 * cs] ? 1 : 0) | (meta[2 * cs + 1] ? 2 : 0);
             mbar_arrive(&bars[T_SCFULL + n % SCS]);
           }
@@ -357,8 +396,8 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
       if (first < n1) unpack_k(first);
       for (n = first; n < n1; n += 2) {
         if (n + 2 < n1) unpack_k(n + 2);   // V(n) may have to wait for PV(n-2); the next S does not
-        const int b = walk.b0 + 2 * (n - start), cs = CST + n % CST, sv = n % VST;
-        wait(T_CFULL + cs, (n / CST) & 1);
+        const int b = walk.b0 + 2 * (n - start), cs = KCST + n % VCST, sv = n % VST;
+        wait(T_CFULL + cs, (n / VCST) & 1);
         const uint8_t* codes = sm + SM::CODES + cs * SM::STEP;
         const bool ok0 = meta[2 * cs] != 0, ok1 = meta[2 * cs + 1] != 0;
         // V: 8 channels of two tokens a lane and turn, a block's turns together
@@ -449,7 +488,6 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
       }
       const int lim = live && p.causal ? max(walk.kv_len - walk.q_len + rr / p.group + 1, 0) : walk.kv_len;
       wait(T_QFULL, piece & 1);
-      const float qs = reinterpret_cast<const float*>(sm + SM::QS)[row] + reinterpret_cast<const float*>(sm + SM::QS)[128 + row];
       // A step's P is taken against a reference R that the steps before the last one left, so the two
       // warpgroups' passes overlap; what O was summed against before (the last step's R) is read at the pass's
       // end.  l is this warpgroup's share of the row's sum, against the reference m it last used.
@@ -457,7 +495,8 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
       for (int n = n0 + ((n0 ^ wg) & 1); n < n1; n += 2) {
         const uint32_t tS = tmem + lane_off + wg * 128, tP = tmem + lane_off + 256 + wg * 64;
         wait(T_SCFULL + n % SCS, (n / SCS) & 1);
-        const float4* s4 = reinterpret_cast<const float4*>(sm + SM::SC) + (n % SCS) * 64;
+        const uint4* s8 = reinterpret_cast<const uint4*>(sm + SM::SC) + (n % SCS) * 16;   // scales of 8 keys
+        f32x2 c2 = pair(p.scale_log2, p.scale_log2);
         const int ok = sc_ok[n % SCS];
         wait(T_SFULL + wg, (n >> 1) & 1);
         if (n == n0 + 1) {   // the piece's first step of the other warpgroup has found a reference
@@ -487,45 +526,48 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
               tmem_wait_ld();
               const int to = (ok >> (q >> 1)) & 1 ? see - q * 32 : 0;
 #pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const float4 s = s4[q * 8 + e / 4], o = s4[32 + q * 8 + e / 4];
-                x[e] = __float_as_uint(to <= e ? -INFINITY : fmaf(__uint_as_float(x[e]), s.x, o.x * qs));
-                x[e + 1] = __float_as_uint(to <= e + 1 ? -INFINITY : fmaf(__uint_as_float(x[e + 1]), s.y, o.y * qs));
-                x[e + 2] = __float_as_uint(to <= e + 2 ? -INFINITY : fmaf(__uint_as_float(x[e + 2]), s.z, o.z * qs));
-                x[e + 3] = __float_as_uint(to <= e + 3 ? -INFINITY : fmaf(__uint_as_float(x[e + 3]), s.w, o.w * qs));
-                top = fmax3(top, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-                top = fmax3(top, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+              for (int e = 0; e < 32; e += 8) {
+                const uint4 s = s8[q * 4 + e / 8];
+                const uint32_t sw[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float a = (__uint_as_float(x[e + 2 * i]) * lo_bf16(sw[i])) * p.scale_log2;
+                  const float b = (__uint_as_float(x[e + 2 * i + 1]) * hi_bf16(sw[i])) * p.scale_log2;
+                  x[e + 2 * i] = __float_as_uint(to <= e + 2 * i ? -INFINITY : a);
+                  x[e + 2 * i + 1] = __float_as_uint(to <= e + 2 * i + 1 ? -INFINITY : b);
+                  top = fmax3(top, __uint_as_float(x[e + 2 * i]), __uint_as_float(x[e + 2 * i + 1]));
+                }
               }
               tmem_st32(tS + q * 32, x);
             }
             tmem_wait_st();
-            s4 = reinterpret_cast<const float4*>(sm + SM::IDENT);
+            s8 = reinterpret_cast<const uint4*>(sm + SM::ONES);
+            c2 = pair(1.f, 1.f);
             if (R == -INFINITY || top > R + 64.f) R = top;
           }
           const float neg = R == -INFINITY ? 0.f : -R;
-          const f32x2 qs2 = pair(qs, qs), neg2 = pair(neg, neg);
+          const f32x2 neg2 = pair(neg, neg);
           float mx0 = -INFINITY, mx1 = -INFINITY;
           f32x2 sum0 = 0ull, sum1 = 0ull;
           uint32_t xa[32], xb[32];
           auto chunk = [&](const uint32_t (&x)[32], int q) {   // P (bf16 pairs) of 32 columns
             uint32_t pk[16];
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const ulonglong2 s = reinterpret_cast<const ulonglong2*>(s4)[q * 8 + e / 4];
-              const ulonglong2 o = reinterpret_cast<const ulonglong2*>(s4)[32 + q * 8 + e / 4];
-              float y0, y1, y2, y3;
-              parts(fma2(pair(x[e], x[e + 1]), s.x, fma2(o.x, qs2, neg2)), y0, y1);
-              parts(fma2(pair(x[e + 2], x[e + 3]), s.y, fma2(o.y, qs2, neg2)), y2, y3);
-              mx0 = fmax3(mx0, y0, y1);
-              mx1 = fmax3(mx1, y2, y3);
-              y0 = ex2_approx(y0);
-              y1 = ex2_approx(y1);
-              y2 = ex2_approx(y2);
-              y3 = ex2_approx(y3);
-              sum0 = add2(sum0, pair(y0, y1));
-              sum1 = add2(sum1, pair(y2, y3));
-              pk[e / 2] = pack_bf16(y0, y1);
-              pk[e / 2 + 1] = pack_bf16(y2, y3);
+            for (int e = 0; e < 32; e += 8) {
+              const uint4 s = s8[q * 4 + e / 8];
+              const uint32_t sw[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float y0, y1;
+                parts(fma2(mul2(pair(x[e + 2 * i], x[e + 2 * i + 1]), pair(sw[i] << 16, sw[i] & 0xFFFF0000u)), c2, neg2), y0, y1);
+                if (i & 1) mx1 = fmax3(mx1, y0, y1);
+                else mx0 = fmax3(mx0, y0, y1);
+                y0 = ex2_approx(y0);
+                y1 = ex2_approx(y1);
+                if (i & 1) sum1 = add2(sum1, pair(y0, y1));
+                else sum0 = add2(sum0, pair(y0, y1));
+                pk[e / 2 + i] = pack_bf16(y0, y1);
+              }
             }
             tmem_st16(tP + q * 16, pk);
           };

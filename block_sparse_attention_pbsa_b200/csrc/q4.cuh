@@ -75,6 +75,8 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
   return d;
 }
+// x - (the bf16 nearest x): what the next term of a split into bf16 terms holds
+__device__ __forceinline__ float bf16_rest(float x) { return x - __bfloat162float(__float2bfloat16_rn(x)); }
 // the neighbouring bf16 on the asked side, as fp32 bits
 __device__ __forceinline__ float bf16_down(float x) {
   uint32_t u = __float_as_uint(x);
