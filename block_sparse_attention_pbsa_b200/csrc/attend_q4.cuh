@@ -9,8 +9,8 @@
 namespace pbsa {
 
 constexpr int Q4_MAX_CTAS = 640;      // of a grid of the few-rows kernel (16 rows a piece)
-constexpr int Q4_TC_MAX_CTAS = 160;   // of a grid of the tensor-core kernel (128 rows a piece)
-constexpr int Q4_PART_ROWS = 2 * (Q4_MAX_CTAS * 16 > Q4_TC_MAX_CTAS * 128 ? Q4_MAX_CTAS * 16 : Q4_TC_MAX_CTAS * 128);
+constexpr int Q4_TC_MAX_CTAS = 160;   // of a grid of the tensor-core kernel (256 rows a piece)
+constexpr int Q4_PART_ROWS = 2 * (Q4_MAX_CTAS * 16 > Q4_TC_MAX_CTAS * 256 ? Q4_MAX_CTAS * 16 : Q4_TC_MAX_CTAS * 256);
 constexpr int Q4_TC_ROWS = 48;        // requests with more rows go to the tensor-core kernel
 
 // A tile that starts in this CTA and ends in a later one (pieces = 0: none).

@@ -2,11 +2,12 @@
 // 5th-generation tensor cores.
 //
 // The mathematics is attend_q4.cu's.  128 rows (row = token * group + head of the group, so the heads that
-// share a kv head share its keys) fill one M = 128 tile, and every cached byte is used 128 times per tile:
-// the products and the exponentials bound it, and unpacking the codes must hide behind them.
-//  * Work: the line of attend_q4.cuh, with tiles of 128 rows; one CTA per SM, pieces one after another.
-//    With the causal rule a tile is charged what it sees, so long prompts are spread evenly.
-//  * Each step covers two blocks (128 keys).  Warp 0 brings the slots' bytes into a ring with bulk copies;
+// share a kv head share its keys) fill one M = 128 tile, and every cached byte is used for all rows of a
+// tile: the products, the exponentials and the unpacking of the codes bound it.
+//  * Work: the line of attend_q4.cuh, with tiles of 256 rows in two halves, so that a key unpacked once serves
+//    both; one CTA per SM, pieces one after another (one warp walks them and tells the others).  With the causal rule
+//    a tile is charged what it sees, so long prompts are spread evenly.
+//  * Each step covers two blocks (128 keys).  One thread each brings K's and V's bytes with bulk copies;
 //    two warpgroups, alternate steps, unpack them into shared-memory operand tiles (128-byte swizzle): K as
 //    the codes themselves (plus 128, exact in bf16), V as bf16 values s*c + m, rounded once, the bits that
 //    pbsa_expand_q4 gives.  The scores carry no rounding of K (to bf16 it would put 2^-8 |q . k| / sqrt(d) of
@@ -15,17 +16,16 @@
 //    The bracket is one product: (m / s - 128) and sum(q) as three bf16 terms each make a further slice of 16
 //    columns of K and Q.  The scale is applied to the scores in fp32; the softmax reads it as bf16, eight
 //    keys a load, since what every lane of a warp reads from shared memory costs as much as distinct data.
-//  * TMEM: two S, two P (bf16) and one O (512 columns at D = 128); two softmax warpgroups on alternate steps, two
-//    MMA-issuing threads, one for each.  QK(i+2) is issued as soon as S(i) has been read, ahead of PV(i).
-//    The softmax makes one pass over a step's scores: scale, exponential, sum and maximum together, against
-//    the reference that the steps before the last one left, so the two warpgroups' passes overlap.  A step
-//    whose maximum exceeds it by 2^8 moves the reference for a later one (O is rescaled then); P of the step
-//    itself may be as large as 2^64, above which the pass is done again from S.
+//  * The halves take turns on the tensor pipe: while one's scores are exponentiated (a warpgroup each, a row
+//    a thread), the other's P V and next Q K^T run.  TMEM: S and O of each half (512 columns at D = 128), P as
+//    bf16 over S; S(i+1) is issued behind PV(i) by the half's own thread.
+//  * The softmax makes one pass over a step's scores: scale, exponential, sum and maximum together, against the
+//    reference that the steps before left; P waits in registers, so the pass can be repeated from S where
+//    scores exceed the reference by 2^64.  Above 2^8 the reference moves for the next step (O is rescaled then).
 //  * All barriers are used once per step with a step count that runs on over the pieces (a piece without
-//    blocks takes part in none).  The ring of key scales has four places: step n's are
-//    written once QK(n-2) is done, which follows the softmax of step n-4.
-//  * The codes of K and of V have a ring each, so that a step's K can be unpacked before the V of the step
-//    two earlier, which may have to wait for its place.
+//    blocks takes part in none; a half without rows in none of its own.  A thread that
+//    waits on a barrier waits on each of its completions, as a parity tells only neighbours apart).  The ring of key scales has four places:
+//    step n's are written once QK(n-2) is done, which follows the softmax of step n-3.
 //  * Keys that a row does not see get x = -inf by a select after the scale is applied, and V of tokens
 //    that are not cached is zero, so whatever bytes lie there reach no row.
 // Waits are bounded; on expiry the error is recorded and every role runs through its pieces without
@@ -38,17 +38,17 @@ namespace pbsa {
 namespace {
 
 constexpr int TQ_THREADS = 640;      // warpgroups: control, unpack x 2, softmax x 2
+constexpr int TQ_ROWS = 256;         // two halves of 128
 constexpr int TQ_MIN_STEPS = 8;      // blocks that are worth a CTA of their own
-constexpr int KCST = 3, VCST = 2, KST = 2, VST = 2, SCS = 4;   // code rings, operand stages, key scales
+constexpr int STAGES = 2, SCS = 4;   // operand stages of K and of V, key scales
 constexpr uint32_t REG_CTRL = 48, REG_UNPACK = 80, REG_SOFT = 136;   // launched with 96: 48 + 2*80 + 2*136 = 5*96
 static_assert(REG_CTRL + 2 * REG_UNPACK + 2 * REG_SOFT <= 5 * 96, "register split exceeds the launch");
 
-enum { T_QFULL = 0, T_CFULL = 1, T_CEMPTY = T_CFULL + KCST + VCST,   // codes: K ring, then V ring
-       T_KFULL = T_CEMPTY + KCST + VCST,
-       T_KEMPTY = T_KFULL + KST,
-       T_VFULL = T_KEMPTY + KST, T_VEMPTY = T_VFULL + VST, T_SCFULL = T_VEMPTY + VST, T_SFULL = T_SCFULL + SCS,
-       T_PFULL = T_SFULL + 2, T_PVDONE = T_PFULL + 2, T_MMADONE = T_PVDONE + 2, T_XDONE = T_MMADONE + 1,
-       T_WFULL = T_XDONE + 2, T_WEMPTY = T_WFULL + 2, T_BARS = T_WEMPTY + 2 };
+enum { T_QFULL = 0, T_CFULL = 1,                                    // codes: of K for either warpgroup, of V
+       T_CEMPTY = T_CFULL + 4,                                      // of K, of V
+       T_KFULL = T_CEMPTY + 2, T_KEMPTY = T_KFULL + STAGES, T_VFULL = T_KEMPTY + STAGES, T_VEMPTY = T_VFULL + STAGES,
+       T_SCFULL = T_VEMPTY + STAGES, T_SFULL = T_SCFULL + SCS, T_PFULL = T_SFULL + 2, T_MMADONE = T_PFULL + 2,   // of a half
+       T_WFULL = T_MMADONE + 2, T_WEMPTY = T_WFULL + 2, T_BARS = T_WEMPTY + 2 };
 constexpr int WARPS_TOLD = 19;       // warps that read the pieces: all but the one that walks them
 
 // A piece of the CTA's share, as the walking warp passes it on.
@@ -61,22 +61,19 @@ struct TqSmem {
   static constexpr uint32_t PANELS = D / 64;
   static constexpr uint32_t TILE = PANELS * 16384;                  // 128 rows of 64 columns a panel
   static constexpr uint32_t STEP = 2 * Q4<D>::HALF;                 // two blocks' K codes, or V codes
-  static constexpr uint32_t Q = 0;
-  static constexpr uint32_t K = TILE;
-  static constexpr uint32_t V = K + KST * TILE;
-  static constexpr uint32_t QX = V + VST * TILE;                    // 16 more columns of Q: [16 groups of 8 rows][2][8][8]
-  static constexpr uint32_t KX = QX + 4096;                         // ... and of each K stage
-  static constexpr uint32_t CODES = KX + KST * 4096;                // the ring of K codes, then that of V codes
-  static constexpr uint32_t SC = CODES + (KCST + VCST) * STEP;      // bf16 [SCS][128]: scales of the step's keys
-  static constexpr uint32_t QS = SC + SCS * 256;                    // float [128]: sums of a half of Q's rows
-  static constexpr uint32_t MREF = QS + 512;                       // float2 [128]
-  static constexpr uint32_t RLAST = MREF + 1024;                    // float [128]
-  static constexpr uint32_t STAT = RLAST + 512;                     // float2 [2][128]
-  static constexpr uint32_t ONES = STAT + 2048;                     // bf16 [128]: scales of scores that have theirs
+  static constexpr uint32_t Q = 0;                                  // two halves
+  static constexpr uint32_t K = 2 * TILE;
+  static constexpr uint32_t V = K + STAGES * TILE;
+  static constexpr uint32_t QX = V + STAGES * TILE;                 // 8 more columns of Q's halves: [128 rows][8] bf16
+  static constexpr uint32_t KX = QX + 2 * 2048;                     // ... of each K stage
+  static constexpr uint32_t ZERO = KX + STAGES * 2048;              // ... and 8 of zeros behind either
+  static constexpr uint32_t CODES = ZERO + 2048;                    // a step's K codes, and its V codes
+  static constexpr uint32_t SC = CODES + 2 * STEP;                  // bf16 [SCS][128]: scales of the step's keys
+  static constexpr uint32_t ONES = SC + SCS * 256;                  // bf16 [128]: scales of scores that have theirs
   static constexpr uint32_t BARS = ONES + 256;
   static constexpr uint32_t WALK = BARS + T_BARS * 8;               // TqPiece [2]
-  static constexpr uint32_t META = WALK + 2 * sizeof(TqPiece);      // int [rings][2], int [SCS], TMEM address, abort flag
-  static constexpr uint32_t TOTAL = META + 4 * (2 * (KCST + VCST) + SCS + 2);
+  static constexpr uint32_t META = WALK + 2 * sizeof(TqPiece);      // int [2][2], int [SCS], TMEM address, abort flag
+  static constexpr uint32_t TOTAL = META + 4 * (4 + SCS + 2);
   static constexpr uint32_t BYTES = TOTAL + 1024;
 };
 static_assert(TqSmem<128>::BYTES <= 232448, "shared memory");
@@ -118,12 +115,19 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
   return r;
 }
 
-// Shared-memory matrix descriptor of 16 columns without swizzle: 8 x 8 blocks of 128 bytes, 128 bytes apart along
-// the columns, 256 along the rows (QX, KX).
-__device__ __forceinline__ uint64_t plain_desc(uint32_t smem_addr) {
-  return (uint64_t)((smem_addr & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 16 | (uint64_t)(256 >> 4) << 32 | (uint64_t)1 << 46;
+// Shared-memory matrix descriptor of 16 columns without swizzle: two blocks of 8 columns, 16 bytes a row, the second
+// `next` bytes behind the first.
+__device__ __forceinline__ uint64_t plain_desc(uint32_t smem_addr, uint32_t next) {
+  return (uint64_t)((smem_addr & 0x3FFFFu) >> 4) | (uint64_t)(next >> 4) << 16 | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
 }
-__device__ __forceinline__ uint32_t plain_row(int row) { return (row >> 3) * 256 + (row & 7) * 16; }
+// 16 columns of 32 lanes (see tmem_ld32)
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
 
 template <int D>
 __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const AttendQ4Params p) {
@@ -132,25 +136,25 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + SM::BARS);
-  volatile int* meta = reinterpret_cast<volatile int*>(sm + SM::META);          // [KCST + VCST][2]: the block is there
-  volatile int* sc_ok = meta + 2 * (KCST + VCST);                                         // [SCS]: the same, two bits
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + SM::META) + 2 * (KCST + VCST) + SCS;
-  volatile int* abort_flag = meta + 2 * (KCST + VCST) + SCS + 1;
+  volatile int* meta = reinterpret_cast<volatile int*>(sm + SM::META);          // [2][2]: the block is there (K, V)
+  volatile int* sc_ok = meta + 4;                                         // [SCS]: the same, two bits
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + SM::META) + 4 + SCS;
+  volatile int* abort_flag = meta + 4 + SCS + 1;
   __shared__ Q4Start start_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
     for (int i = 0; i < T_BARS; ++i) {
-      const bool many = (i >= T_CEMPTY && i < T_KEMPTY) || (i >= T_VFULL && i < T_VEMPTY) ||
-                        (i >= T_SCFULL && i < T_SFULL) || (i >= T_PFULL && i < T_PVDONE) || (i >= T_XDONE && i < T_WFULL);
-      mbar_init(&bars[i], many ? 128 : i == T_QFULL ? 256 : i == T_MMADONE ? 2 : i >= T_WEMPTY ? WARPS_TOLD : 1);
+      const bool full = i == T_CEMPTY || i == T_CEMPTY + 1 || (i >= T_KFULL && i < T_KEMPTY) || (i >= T_VFULL && i < T_VEMPTY) ||
+                        (i >= T_SCFULL && i < T_SFULL) || (i >= T_PFULL && i < T_MMADONE);
+      const bool both = (i >= T_KEMPTY && i < T_VFULL) || (i >= T_VEMPTY && i < T_SCFULL);
+      mbar_init(&bars[i], full ? 128 : both ? 2 : i == T_QFULL ? 256 : i >= T_WEMPTY ? WARPS_TOLD : 1);
     }
     *abort_flag = 0;
     fence_barrier_init();
   }
   if (tid < 64) reinterpret_cast<uint32_t*>(sm + SM::ONES)[tid] = 0x3F803F80u;
-  // the columns behind the six that are written stay zero
-  for (int i = tid; i < (1 + KST) * 1024; i += TQ_THREADS) reinterpret_cast<uint32_t*>(sm + SM::QX)[i] = 0u;
+  if (tid < 512) reinterpret_cast<uint32_t*>(sm + SM::ZERO)[tid] = 0u;
   fence_proxy_async_smem();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == 1) {
@@ -158,7 +162,7 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
     tmem_relinquish();
   }
   tc_fence_before();
-  const Q4Share share = q4_share<TQ_THREADS>(p, 128, TQ_MIN_STEPS, &start_s);   // has block barriers
+  const Q4Share share = q4_share<TQ_THREADS>(p, TQ_ROWS, TQ_MIN_STEPS, &start_s);   // has block barriers
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   auto wait = [&](int bar, uint32_t parity) {
@@ -183,7 +187,7 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
     if (warp == 2) {
       // ------------------------------------------------------------- walks the share
       if (lane == 0) {
-        Q4Walk walk(p, share, 128);
+        Q4Walk walk(p, share, TQ_ROWS);
         bool more = true;
         for (int k = 0; more; ++k) {
           more = walk.next();
@@ -198,7 +202,7 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
     }
     if (warp == 0) {
       // ------------------------------------------------------------- slots' bytes
-      int n = 0;   // step (lane 0 brings K codes, lane 1 V codes, each at its ring's pace)
+      int n = 0;   // step (lane 0 brings K codes, lane 1 V codes, each at its own pace)
       for (int k = 0;; ++k) {
         const TqPiece walk = told(k);
         if (!walk.more) break;
@@ -212,8 +216,8 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
             const bool has1 = b + 1 < walk.b1;
             if (b + 2 < walk.b1) next0 = __ldg(row + b + 2);
             if (b + 3 < walk.b1) next1 = __ldg(row + b + 3);
-            const int depth = lane ? VCST : KCST, cs = lane * KCST + n % depth;
-            wait(T_CEMPTY + cs, ((n / depth) & 1) ^ 1);
+            const int cs = lane;
+            wait(T_CEMPTY + cs, (n & 1) ^ 1);
             if (*abort_flag) break;
             const bool ok0 = slot0 >= 0 && slot0 < p.pool_slots, ok1 = has1 && slot1 >= 0 && slot1 < p.pool_slots;
             if (!ok0) record_error(p.ws, PBSA_ERR_DEVICE_INDEX, slot0, K_Q4_ATTEND);
@@ -222,78 +226,86 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
             meta[2 * cs + 1] = ok1;
             uint8_t* dst = sm + SM::CODES + cs * SM::STEP;
             const uint32_t bytes = (ok0 ? Q::HALF : 0) + (ok1 ? Q::HALF : 0);
-            if (bytes > 0) mbar_arrive_expect_tx(&bars[T_CFULL + cs], bytes);
-            else mbar_arrive(&bars[T_CFULL + cs]);
-            if (ok0) bulk_load(dst, src + (size_t)slot0 * Q::BYTES, Q::HALF, &bars[T_CFULL + cs]);
-            if (ok1) bulk_load(dst + Q::HALF, src + (size_t)slot1 * Q::BYTES, Q::HALF, &bars[T_CFULL + cs]);
+            uint64_t* full = &bars[T_CFULL + 2 * cs + (n & 1)];   // a barrier a warpgroup: neither sees every step
+            if (bytes > 0) mbar_arrive_expect_tx(full, bytes);
+            else mbar_arrive(full);
+            if (ok0) bulk_load(dst, src + (size_t)slot0 * Q::BYTES, Q::HALF, full);
+            if (ok1) bulk_load(dst + Q::HALF, src + (size_t)slot1 * Q::BYTES, Q::HALF, full);
             ++n;
           }
         }
         __syncwarp();
       }
       // the CTA must not end with copies in flight
-      if (lane < 2) {
-        const int depth = lane ? VCST : KCST;
-        for (int i = max(0, n - depth); i < n; ++i)
-          mbar_wait(&bars[T_CFULL + lane * KCST + i % depth], (i / depth) & 1, kWaitLimitNs);
-      }
+      if (lane < 2 && n > 0) mbar_wait(&bars[T_CFULL + 2 * lane + ((n - 1) & 1)], ((n - 1) >> 1) & 1, kWaitLimitNs);
       __syncwarp();
     }
     if (warp == 1 || warp == 3) {
-      // ------------------------------------------------------------- MMA issuers: steps of their parity
+      // ------------------------------------------------------------- MMA issuers, one for each half
       const uint32_t w = warp >> 1;
       {
-        const uint32_t tO = tmem + 384;
-        const uint64_t dq = sw128_desc(smem_u32(sm + SM::Q), 16, 1024);
+        const uint32_t tS = tmem + w * 128, tO = tmem + 256 + w * 128;
+        const uint64_t dq = sw128_desc(smem_u32(sm + SM::Q + w * SM::TILE), 16, 1024);
         const uint64_t dk = sw128_desc(smem_u32(sm + SM::K), 16, 1024);
         const uint64_t dv = sw128_desc(smem_u32(sm + SM::V), 16384, 1024);
-        const uint64_t dqx = plain_desc(smem_u32(sm + SM::QX)), dkx = plain_desc(smem_u32(sm + SM::KX));
+        const uint64_t dqx = plain_desc(smem_u32(sm + SM::QX + w * 2048), SM::ZERO - SM::QX - w * 2048);
         constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, 128, 0, 0), IDESC_PV = idesc_bf16_f32(128, D, 0, 1);
         auto issue_qk = [&](int n) {
-          const int sk = n % KST;
-          wait(T_KFULL + sk, (n / KST) & 1);
+          const int sk = n % STAGES;
+          wait(T_KFULL + sk, (n / STAGES) & 1);
           if (*abort_flag) return;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-            mma_bf16_ss(tmem + w * 128, dq + off, dk + ((sk * SM::TILE) >> 4) + off, IDESC_QK, kk > 0 ? 1u : 0u);
+            mma_bf16_ss(tS, dq + off, dk + ((sk * SM::TILE) >> 4) + off, IDESC_QK, kk > 0 ? 1u : 0u);
           }
-          mma_bf16_ss(tmem + w * 128, dqx, dkx + ((sk * 4096) >> 4), IDESC_QK, 1u);
+          mma_bf16_ss(tS, dqx, plain_desc(smem_u32(sm + SM::KX + sk * 2048), SM::ZERO - SM::KX - sk * 2048), IDESC_QK, 1u);
           mma_commit(&bars[T_SFULL + w]);
           mma_commit(&bars[T_KEMPTY + sk]);
         };
-        int n0 = 0, piece = 0;
+        int n0 = 0, piece = 0, used = 0, done = 0;   // used, done: steps and pieces that this half has taken part in
         for (int k = 0;; ++k) {
           const TqPiece walk = told(k);
           if (!walk.more) break;
           if (walk.b0 == walk.b1) continue;
           const int n1 = n0 + ((walk.b1 - walk.b0 + 1) >> 1);
+          const bool takes_part = w == 0 || walk.rows > walk.mt * TQ_ROWS + 128;
           if (lane == 0) {
             wait(T_QFULL, piece & 1);
-            const int first = n0 + ((n0 ^ (int)w) & 1);
-            if (first < n1) issue_qk(first);
-            for (int n = first; n < n1 && !*abort_flag; n += 2) {
-              const int sv = n % VST;
-              wait(T_PFULL + w, (n >> 1) & 1);           // S(n) has been read, P(n) written
-              if (n + 2 < n1) issue_qk(n + 2);
-              // PV(n-1) complete first, so that O accumulates in step order
-              if (n > n0) wait(T_PVDONE + (w ^ 1), ((n - 1) >> 1) & 1);
-              wait(T_VFULL + sv, (n / VST) & 1);
-              if (*abort_flag) break;
-              tc_fence_after();
+            if (takes_part) {
+              issue_qk(n0);
+              for (int n = n0; n < n1 && !*abort_flag; ++n) {
+                const int sv = n % STAGES;
+                wait(T_PFULL + w, (used + n - n0) & 1);
+                wait(T_VFULL + sv, (n / STAGES) & 1);
+                if (*abort_flag) break;
+                tc_fence_after();
+                // P(n) lies over S(n): S(n+1) is issued behind its use, in order
 #pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                mma_bf16_ts(tO, tmem + 256 + w * 64 + kk * 8, dv + ((sv * SM::TILE + kk * 2048) >> 4), IDESC_PV,
-                            (n > n0 || kk > 0) ? 1u : 0u);
-              mma_commit(&bars[T_VEMPTY + sv]);
-              mma_commit(&bars[T_PVDONE + w]);
+                for (int kk = 0; kk < 8; ++kk)
+                  mma_bf16_ts(tO, tS + kk * 8, dv + ((sv * SM::TILE + kk * 2048) >> 4), IDESC_PV, (n > n0 || kk > 0) ? 1u : 0u);
+                mma_commit(&bars[T_VEMPTY + sv]);
+                if (n + 1 < n1) issue_qk(n + 1);
+              }
+            } else {
+              for (int n = n0; n < n1 && !*abort_flag; ++n) {   // the stages go round without this half
+                wait(T_KFULL + n % STAGES, (n / STAGES) & 1);
+                mbar_arrive(&bars[T_KEMPTY + n % STAGES]);
+                wait(T_VFULL + n % STAGES, (n / STAGES) & 1);
+                mbar_arrive(&bars[T_VEMPTY + n % STAGES]);
+              }
             }
-            // all MMAs of both issuers: the tile's O is complete, Q and the operand stages are free
-            mma_commit(&bars[T_MMADONE]);
-            mbar_wait(&bars[T_MMADONE], piece & 1, kWaitLimitNs);
+            if (takes_part) {   // all MMAs of this half: its O is complete, its Q is free
+              mma_commit(&bars[T_MMADONE + w]);
+              mbar_wait(&bars[T_MMADONE + w], done & 1, kWaitLimitNs);
+            }
           }
           __syncwarp();
+          if (takes_part) {
+            used += n1 - n0;
+            ++done;
+          }
           n0 = n1;
           ++piece;
         }
@@ -304,47 +316,46 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
     setmaxnreg_dec<REG_UNPACK>();
     // --------------------------------------------------------------- unpack: steps of the warpgroup's parity
     const int ug = (warp - 4) >> 2, t = tid & 127, uw = warp & 3;
-    int n = 0, piece = 0;
+    int n = 0, done0 = 0, done1 = 0;   // pieces that the halves have taken part in
     for (int k = 0;; ++k) {
       const TqPiece walk = told(k);
       if (!walk.more) break;
       if (walk.b0 == walk.b1) continue;
-      // Q: half a row a thread, and its sum
-      if (piece > 0) wait(T_MMADONE, (piece - 1) & 1);
+      // Q: a row a thread, and its sum
+      if (done0 > 0) wait(T_MMADONE, (done0 - 1) & 1);
+      if (done1 > 0) wait(T_MMADONE + 1, (done1 - 1) & 1);
+      ++done0;
+      if (walk.rows > walk.mt * TQ_ROWS + 128) ++done1;
       {
-        const int rr = walk.mt * 128 + t;
+        const int rr = walk.mt * TQ_ROWS + ug * 128 + t;
         const bool live = rr < walk.rows;
         const int tok = live ? rr / p.group : 0, hd = live ? rr - tok * p.group : 0;
         const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
                                                           (long long)(walk.q0 + tok) * p.q_ld +
                                                           (long long)(walk.h * p.group + hd) * D);
+        uint8_t* dst = sm + SM::Q + ug * SM::TILE + t * 128;
         float sum = 0.f;
 #pragma unroll 4
-        for (int c = ug * (D / 16); c < (ug + 1) * (D / 16); ++c) {
+        for (int c = 0; c < D / 8; ++c) {
           const uint4 v = live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
           const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) sum += lo_bf16(u[i]) + hi_bf16(u[i]);
-          *reinterpret_cast<uint4*>(sm + SM::Q + (c >> 3) * 16384 + t * 128 + (((c & 7) ^ (t & 7)) << 4)) = v;
+          *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + (((c & 7) ^ (t & 7)) << 4)) = v;
         }
         // the row's sum as three bf16 terms, beside which a key has three of its offset: columns
         // (1, 2, 3, 1, 2, 1) of the one against (1, 1, 1, 2, 2, 3) of the other
-        if (ug == 1) reinterpret_cast<float*>(sm + SM::QS)[t] = sum;
-        asm volatile("bar.sync 2, 256;" ::: "memory");
-        if (ug == 0) {
-          sum += reinterpret_cast<const float*>(sm + SM::QS)[t];
-          const float s2 = bf16_rest(sum), s3 = bf16_rest(s2);
-          *reinterpret_cast<uint4*>(sm + SM::QX + plain_row(t)) =
-              make_uint4(pack_bf16(sum, s2), pack_bf16(s3, sum), pack_bf16(s2, sum), 0u);
-        }
+        const float s2 = bf16_rest(sum), s3 = bf16_rest(s2);
+        *reinterpret_cast<uint4*>(sm + SM::QX + ug * 2048 + t * 16) =
+            make_uint4(pack_bf16(sum, s2), pack_bf16(s3, sum), pack_bf16(s2, sum), 0u);
         fence_proxy_async_smem();
         mbar_arrive(&bars[T_QFULL]);
       }
       const int n1 = n + ((walk.b1 - walk.b0 + 1) >> 1), start = n, first = n + ((n ^ ug) & 1);
       auto unpack_k = [&](int n) {
-        const int cs = n % KCST, sk = n % KST;
-        wait(T_CFULL + cs, (n / KCST) & 1);
-        const uint8_t* codes = sm + SM::CODES + cs * SM::STEP;
+        const int sk = n % STAGES;
+        wait(T_CFULL + ug, (n >> 1) & 1);
+        const uint8_t* codes = sm + SM::CODES;
         // K: 16 (D = 64: 8) code bytes a lane; 8 lanes write 4 rows of two neighbouring column groups, 8
         // different 16-byte columns after the swizzle.  All of a thread's codes are read before the first is used.
         {
@@ -364,20 +375,22 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
             }
           }
           uint8_t* dst = sm + SM::K + sk * SM::TILE + ((j * W) >> 3) * 16384 + row0 * 128;
-          wait(T_KEMPTY + sk, ((n / KST) & 1) ^ 1);   // QK(n-2) is done, and before it the softmax of step n-4
+          const uint32_t ksm = *reinterpret_cast<const uint32_t*>(codes + (t >> 6) * Q::HALF + Q::OFF_KS + (t & 63) * 4);
+          const int there = (meta[0] ? 1 : 0) | (meta[1] ? 2 : 0);
+          mbar_arrive(&bars[T_CEMPTY]);
+          wait(T_KEMPTY + sk, ((n / STAGES) & 1) ^ 1);   // QK(n-2) is done, and before it the softmax of step n-3
           {   // key t: its scale, and what the sum of the row is multiplied by (see the top of the file)
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + (t >> 6) * Q::HALF + Q::OFF_KS + (t & 63) * 4);
-            const float m = hi_bf16(w);
-            float s = lo_bf16(w);
+            const float m = hi_bf16(ksm);
+            float s = lo_bf16(ksm);
             // a scale that is nothing beside the minimum (0: all channels are m): the minimum alone, scaled by itself
             if (s <= fabsf(m) * 0x1p-60f) s = m == 0.f ? 1.f : fabsf(m);
             const float r = __fdiv_rn(m, s) - 128.f;
             const float r2 = bf16_rest(r), r3 = bf16_rest(r2);
             const uint32_t r11 = pack_bf16(r, r);
-            *reinterpret_cast<uint4*>(sm + SM::KX + sk * 4096 + plain_row(t)) =
+            *reinterpret_cast<uint4*>(sm + SM::KX + sk * 2048 + t * 16) =
                 make_uint4(r11, pack_bf16(r, r2), pack_bf16(r2, r3), 0u);
             reinterpret_cast<uint16_t*>(sm + SM::SC)[(n % SCS) * 128 + t] = (uint16_t)(__float_as_uint(s) >> 16);
-            if (t == 0) sc_ok[n % SCS] = (meta[2 * cs] ? 1 : 0) | (meta[2 * cs + 1] ? 2 : 0);
+            if (t == 0) sc_ok[n % SCS] = there;
             mbar_arrive(&bars[T_SCFULL + n % SCS]);
           }
 #pragma unroll
@@ -390,16 +403,15 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
           }
           fence_proxy_async_smem();
           mbar_arrive(&bars[T_KFULL + sk]);
-          mbar_arrive(&bars[T_CEMPTY + cs]);
         }
       };
       if (first < n1) unpack_k(first);
       for (n = first; n < n1; n += 2) {
         if (n + 2 < n1) unpack_k(n + 2);   // V(n) may have to wait for PV(n-2); the next S does not
-        const int b = walk.b0 + 2 * (n - start), cs = KCST + n % VCST, sv = n % VST;
-        wait(T_CFULL + cs, (n / VCST) & 1);
-        const uint8_t* codes = sm + SM::CODES + cs * SM::STEP;
-        const bool ok0 = meta[2 * cs] != 0, ok1 = meta[2 * cs + 1] != 0;
+        const int b = walk.b0 + 2 * (n - start), sv = n % STAGES;
+        wait(T_CFULL + 2 + ug, (n >> 1) & 1);
+        const uint8_t* codes = sm + SM::CODES + SM::STEP;
+        const bool ok0 = meta[2] != 0, ok1 = meta[3] != 0;
         // V: 8 channels of two tokens a lane and turn, a block's turns together
         {
           constexpr int HALVES = D / 64;                // 8-channel halves of a lane's bytes in the layout
@@ -428,7 +440,8 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
                 if (row0 + i * GROUPS * 8 + 1 >= left) sc[i].y = 0u;
               }
             }
-            if (half == 0) wait(T_VEMPTY + sv, ((n / VST) & 1) ^ 1);
+            if (half == 1) mbar_arrive(&bars[T_CEMPTY + 1]);   // all codes have been read
+            if (half == 0) wait(T_VEMPTY + sv, ((n / STAGES) & 1) ^ 1);
 #pragma unroll
             for (int i = 0; i < TURNS; ++i) {
               const uint32_t s0 = __byte_perm(sc[i].x, 0, 0x1010), m0 = __byte_perm(sc[i].x, 0, 0x3232);
@@ -451,69 +464,59 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
           fence_proxy_async_smem();
           mbar_arrive(&bars[T_VFULL + sv]);
         }
-        mbar_arrive(&bars[T_CEMPTY + cs]);
       }
       n = n1;
-      ++piece;
     }
   } else {
     setmaxnreg_inc<REG_SOFT>();
-    // --------------------------------------------------------------- softmax
-    const int wg = (warp - 12) >> 2;         // steps of this parity
+    // --------------------------------------------------------------- softmax, a warpgroup for each half
+    const int half = (warp - 12) >> 2;
     const int wq = warp & 3;                 // TMEM lane quadrant this warp may access
-    const int row = wq * 32 + lane;
+    const int row = wq * 32 + lane;          // of the half
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
-    const uint32_t tO = tmem + lane_off + 384;
-    float2* mref = reinterpret_cast<float2*>(sm + SM::MREF);   // (the last step's reference, the one it proposes)
-    int n0 = 0, piece = 0;
+    const uint32_t tS = tmem + lane_off + half * 128, tO = tmem + lane_off + 256 + half * 128;
+    int n0 = 0, used = 0, done = 0;
     for (int k = 0;; ++k) {
       const TqPiece walk = told(k);
       if (!walk.more) break;
       const int n1 = n0 + ((walk.b1 - walk.b0 + 1) >> 1);
-      const int rr = walk.mt * 128 + row;
-      const bool live = rr < walk.rows;
+      const int rr = walk.mt * TQ_ROWS + half * 128 + row;
+      const bool live = rr < walk.rows, takes_part = half == 0 || walk.rows > walk.mt * TQ_ROWS + 128;
       if (walk.b0 == walk.b1) {   // nothing to see: no other role takes part
-        if (wg == 0 && live) {
+        if (live) {
           const float zero[4] = {0.f, 0.f, 0.f, 0.f};
           for (int ch = 0; ch < D; ch += 4) {
             if (walk.piece < 0)
               q4_write_row<D>(p, walk.q0, rr, walk.h, ch, zero, -INFINITY, 0.f, ch == 0);
             else
-              *reinterpret_cast<float4*>(p.part_o + ((size_t)walk.piece * p.part_rows + row) * D + ch) =
+              *reinterpret_cast<float4*>(p.part_o + ((size_t)walk.piece * p.part_rows + half * 128 + row) * D + ch) =
                   make_float4(0.f, 0.f, 0.f, 0.f);
           }
-          if (walk.piece >= 0) p.part_ml[(size_t)walk.piece * p.part_rows + row] = make_float2(-INFINITY, 0.f);
+          if (walk.piece >= 0) p.part_ml[(size_t)walk.piece * p.part_rows + half * 128 + row] = make_float2(-INFINITY, 0.f);
         }
         continue;
       }
+      // l and O are sums against the reference M; R is the next step's
+      float M = -INFINITY, R = -INFINITY, l = 0.f;
       const int lim = live && p.causal ? max(walk.kv_len - walk.q_len + rr / p.group + 1, 0) : walk.kv_len;
-      wait(T_QFULL, piece & 1);
-      // A step's P is taken against a reference R that the steps before the last one left, so the two
-      // warpgroups' passes overlap; what O was summed against before (the last step's R) is read at the pass's
-      // end.  l is this warpgroup's share of the row's sum, against the reference m it last used.
-      float m = -INFINITY, l = 0.f, T = -INFINITY;   // T: reference of this warpgroup's next step
-      for (int n = n0 + ((n0 ^ wg) & 1); n < n1; n += 2) {
-        const uint32_t tS = tmem + lane_off + wg * 128, tP = tmem + lane_off + 256 + wg * 64;
+      for (int n = n0; takes_part && n < n1; ++n, ++used) {
+        wait(T_SFULL + half, used & 1);
+        // (complete by now; waited for only after S, as this half may have skipped pieces and so completions)
         wait(T_SCFULL + n % SCS, (n / SCS) & 1);
         const uint4* s8 = reinterpret_cast<const uint4*>(sm + SM::SC) + (n % SCS) * 16;   // scales of 8 keys
         f32x2 c2 = pair(p.scale_log2, p.scale_log2);
         const int ok = sc_ok[n % SCS];
-        wait(T_SFULL + wg, (n >> 1) & 1);
-        if (n == n0 + 1) {   // the piece's first step of the other warpgroup has found a reference
-          wait(T_XDONE + (wg ^ 1), ((n - 1) >> 1) & 1);
-          T = mref[row].y;
-        }
         if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
         tc_fence_after();
         const int see = lim - (walk.b0 + 2 * (n - n0)) * BT;    // of the step's keys
-        if (n - 2 >= n0) wait(T_PVDONE + wg, ((n - 2) >> 1) & 1);   // P(n-2), in the same columns, has been used
-        float R = T, alpha = 1.f, top = -INFINITY, psum;
+        float top = -INFINITY, psum;
+        uint32_t pk[64];
         // Plain: one pass over S.  Careful, where keys are masked, where no key has been seen yet, where R is so
         // large that its rounding in the fused product would count, and where a plain pass has met scores above
         // R + 64 (P could pass its range): x is first written over S and its maximum found, R moves up to it if
         // need be, and the maximum less itself is zero however large it is.
         bool careful = __any_sync(0xffffffffu, see < 128 || R == -INFINITY || fabsf(R) > 4096.f) || ok != 3;
-        bool plain = true, joined = n == n0;
+        bool plain = true;
 #pragma unroll 1
         while (true) {
           if (careful && plain) {
@@ -549,73 +552,49 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
           const f32x2 neg2 = pair(neg, neg);
           float mx0 = -INFINITY, mx1 = -INFINITY;
           f32x2 sum0 = 0ull, sum1 = 0ull;
-          uint32_t xa[32], xb[32];
-          auto chunk = [&](const uint32_t (&x)[32], int q) {   // P (bf16 pairs) of 32 columns
-            uint32_t pk[16];
+          uint32_t x[2][16];
+          tmem_ld16(tS, x[0]);
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              const uint4 s = s8[q * 4 + e / 8];
+          for (int q = 0; q < 8; ++q) {
+            tmem_wait_ld();
+            if (q < 7) tmem_ld16(tS + (q + 1) * 16, x[(q + 1) & 1]);   // in flight behind this chunk
+#pragma unroll
+            for (int e = 0; e < 16; e += 8) {
+              const uint4 s = s8[q * 2 + e / 8];
               const uint32_t sw[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 float y0, y1;
-                parts(fma2(mul2(pair(x[e + 2 * i], x[e + 2 * i + 1]), pair(sw[i] << 16, sw[i] & 0xFFFF0000u)), c2, neg2), y0, y1);
+                parts(fma2(mul2(pair(x[q & 1][e + 2 * i], x[q & 1][e + 2 * i + 1]), pair(sw[i] << 16, sw[i] & 0xFFFF0000u)),
+                           c2, neg2), y0, y1);
                 if (i & 1) mx1 = fmax3(mx1, y0, y1);
                 else mx0 = fmax3(mx0, y0, y1);
                 y0 = ex2_approx(y0);
                 y1 = ex2_approx(y1);
                 if (i & 1) sum1 = add2(sum1, pair(y0, y1));
                 else sum0 = add2(sum0, pair(y0, y1));
-                pk[e / 2 + i] = pack_bf16(y0, y1);
+                pk[q * 8 + e / 2 + i] = pack_bf16(y0, y1);
               }
             }
-            tmem_st16(tP + q * 16, pk);
-          };
-          tmem_ld32(tS, xa);
-#pragma unroll 1
-          for (int q = 0; q < 4; q += 2) {                     // the next columns in flight
-            tmem_wait_ld();
-            tmem_ld32(tS + (q + 1) * 32, xb);
-            chunk(xa, q);
-            tmem_wait_ld();
-            if (q == 0) tmem_ld32(tS + 64, xa);
-            chunk(xb, q + 1);
           }
           {
             float a, b;
             parts(add2(sum0, sum1), a, b);
             psum = a + b;
           }
-          if (plain) {
-            const float mx = fmaxf(mx0, mx1);
-            top = mx - neg;
-            if (__any_sync(0xffffffffu, mx > 64.f)) {
-              careful = true;
-              continue;
-            }
-          }
-          if (joined) break;
-          // What O was summed against (v.x), and the reference that the last step proposes.  If that step met far
-          // larger scores, this step's P is taken against its reference instead.
-          joined = true;
-          wait(T_XDONE + (wg ^ 1), ((n - 1) >> 1) & 1);
-          const float2 v = mref[row];
-          T = v.y;
-          alpha = v.x;
-          const bool again = v.x > R + 64.f && R != -INFINITY;
-          if (again || R == -INFINITY) R = v.x;
-          if (!__any_sync(0xffffffffu, again)) break;
+          if (!plain) break;
+          const float mx = fmaxf(mx0, mx1);
+          top = mx - neg;
+          if (!__any_sync(0xffffffffu, mx > 64.f)) break;
+          careful = true;
         }
-        if (n > n0) alpha = alpha == R || alpha == -INFINITY ? 1.f : ex2_approx(alpha - R);
-        T = fmaxf(T, top > R + 8.f ? top : R);
-        mref[row] = make_float2(R, T);
-        mbar_arrive(&bars[T_XDONE + wg]);
-        if (m != -INFINITY && m != R) l *= ex2_approx(m - R);
-        m = R;
-        l += psum;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_st16(tS + q * 16, pk + q * 16);
+        // l and O go to this step's reference (S(n) follows PV(n-1), so O is at rest)
+        const float alpha = M == R || M == -INFINITY ? 1.f : ex2_approx(M - R);
+        l = fmaf(l, alpha, psum);
+        M = R;
         if (n > n0 && __any_sync(0xffffffffu, alpha != 1.f)) {     // tcgen05.ld/st are warp-collective
-          wait(T_PVDONE + ((n - 1) & 1), ((n - 1) >> 1) & 1);
-          tc_fence_after();
 #pragma unroll 1
           for (int q = 0; q < D / 32; ++q) {
             uint32_t ov[32];
@@ -626,45 +605,40 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
             tmem_st32(tO + q * 32, ov);
           }
         }
+        if (top > R + 8.f) R = top;
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&bars[T_PFULL + wg]);
-        if (n + 1 == n1) reinterpret_cast<float*>(sm + SM::RLAST)[row] = R;   // what O is against
+        mbar_arrive(&bars[T_PFULL + half]);
       }
       // ------------------------------------------------------------- the piece's end
-      wait(T_MMADONE, piece & 1);
-      float2* stat = reinterpret_cast<float2*>(sm + SM::STAT);
-      stat[wg * 128 + row] = make_float2(m, l);
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      const float2 st0 = stat[row], st1 = stat[128 + row];
-      const float M = reinterpret_cast<const float*>(sm + SM::RLAST)[row];
-      const float L = st0.y * q4_weight(st0.x, M) + st1.y * q4_weight(st1.x, M);
-      tc_fence_after();
+      if (takes_part) {
+        wait(T_MMADONE + half, done & 1);
+        tc_fence_after();
+        ++done;
 #pragma unroll 1
-      for (int q = 0; q < D / 64; ++q) {                 // this warpgroup's half of the channels
-        const int ch = wg * (D / 2) + q * 32;
-        uint32_t ov[32];
-        tmem_ld32(tO + ch, ov);
-        tmem_wait_ld();
-        if (live && !*abort_flag) {
+        for (int q = 0; q < D / 32; ++q) {
+          uint32_t ov[32];
+          tmem_ld32(tO + q * 32, ov);
+          tmem_wait_ld();
+          if (live && !*abort_flag) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float acc[4] = {__uint_as_float(ov[e]), __uint_as_float(ov[e + 1]), __uint_as_float(ov[e + 2]),
-                                  __uint_as_float(ov[e + 3])};
-            if (walk.piece < 0)
-              q4_write_row<D>(p, walk.q0, rr, walk.h, ch + e, acc, M, L, ch + e == 0);
-            else
-              *reinterpret_cast<float4*>(p.part_o + ((size_t)walk.piece * p.part_rows + row) * D + ch + e) =
-                  make_float4(acc[0], acc[1], acc[2], acc[3]);
+            for (int e = 0; e < 32; e += 4) {
+              const int ch = q * 32 + e;
+              const float acc[4] = {__uint_as_float(ov[e]), __uint_as_float(ov[e + 1]), __uint_as_float(ov[e + 2]),
+                                    __uint_as_float(ov[e + 3])};
+              if (walk.piece < 0)
+                q4_write_row<D>(p, walk.q0, rr, walk.h, ch, acc, M, l, ch == 0);
+              else
+                *reinterpret_cast<float4*>(p.part_o + ((size_t)walk.piece * p.part_rows + half * 128 + row) * D + ch) =
+                    make_float4(acc[0], acc[1], acc[2], acc[3]);
+            }
           }
         }
+        if (walk.piece >= 0 && live && !*abort_flag)
+          p.part_ml[(size_t)walk.piece * p.part_rows + half * 128 + row] = make_float2(M, l);
       }
-      if (wg == 0 && walk.piece >= 0 && live && !*abort_flag)
-        p.part_ml[(size_t)walk.piece * p.part_rows + row] = make_float2(M, L);
       tc_fence_before();
-      asm volatile("bar.sync 1, 256;" ::: "memory");      // O, the statistics and the references are free
       n0 = n1;
-      ++piece;
     }
   }
 
@@ -682,7 +656,7 @@ cudaError_t launch_t(AttendQ4Params p, cudaStream_t st) {
   auto kern = attend_q4_tc_kernel<D>;
   cudaError_t e = set_smem_once((const void*)kern, (int)TqSmem<D>::BYTES);
   if (e != cudaSuccess) return e;
-  p.part_rows = 128;
+  p.part_rows = TQ_ROWS;
   int sms = 0, dev = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;

@@ -246,6 +246,8 @@ def test_prompts_and_decodes_together(hq, hk, d, dtype, causal):
     ([(33, 5000)], 1, 1, 128, True),                   # one row tile over every CTA
     ([(513, 700), (0, 3), (2, 4000)], 3, 1, 64, True),
     ([(5, 333), (4, 100)], 64, 1, 128, True),          # 64 heads share one
+    ([(25, 900), (130, 300), (20, 5), (300, 0)], 4, 2, 128, True),   # tiles with and without a second half
+    ([(60, 64), (120, 10), (64, 900), (70, 1)], 2, 1, 64, False),
 ])
 def test_long_prompts(lens, hq, hk, d, causal):
     f = Filled(lens, hq, hk, d, "bf16", seed=14, rows_after=2)
