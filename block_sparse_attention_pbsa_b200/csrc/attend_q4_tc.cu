@@ -48,7 +48,7 @@ enum { T_QFULL = 0, T_CFULL = 1,                                    // codes: of
        T_CEMPTY = T_CFULL + 4,                                      // of K, of V
        T_KFULL = T_CEMPTY + 2, T_KEMPTY = T_KFULL + STAGES, T_VFULL = T_KEMPTY + STAGES, T_VEMPTY = T_VFULL + STAGES,
        T_SCFULL = T_VEMPTY + STAGES, T_SFULL = T_SCFULL + SCS, T_PFULL = T_SFULL + 2, T_MMADONE = T_PFULL + 2,   // of a half
-       T_WFULL = T_MMADONE + 2, T_WEMPTY = T_WFULL + 2, T_BARS = T_WEMPTY + 2 };
+       T_TURN = T_MMADONE + 2, T_WFULL = T_TURN + 2, T_WEMPTY = T_WFULL + 2, T_BARS = T_WEMPTY + 2 };
 constexpr int WARPS_TOLD = 19;       // warps that read the pieces: all but the one that walks them
 
 // A piece of the CTA's share, as the walking warp passes it on.
@@ -129,6 +129,13 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr));
 }
 
+// The wait for tmem_ld16's values, tied to those values alone: arithmetic of other columns may move across it.
+__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
+
 template <int D>
 __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const AttendQ4Params p) {
   using Q = Q4<D>;
@@ -146,7 +153,7 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
   if (tid == 0) {
     for (int i = 0; i < T_BARS; ++i) {
       const bool full = i == T_CEMPTY || i == T_CEMPTY + 1 || (i >= T_KFULL && i < T_KEMPTY) || (i >= T_VFULL && i < T_VEMPTY) ||
-                        (i >= T_SCFULL && i < T_SFULL) || (i >= T_PFULL && i < T_MMADONE);
+                        (i >= T_SCFULL && i < T_SFULL) || (i >= T_PFULL && i < T_MMADONE) || i == T_TURN || i == T_TURN + 1;
       const bool both = (i >= T_KEMPTY && i < T_VFULL) || (i >= T_VEMPTY && i < T_SCFULL);
       mbar_init(&bars[i], full ? 128 : both ? 2 : i == T_QFULL ? 256 : i >= T_WEMPTY ? WARPS_TOLD : 1);
     }
@@ -475,13 +482,13 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
     const int row = wq * 32 + lane;          // of the half
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const uint32_t tS = tmem + lane_off + half * 128, tO = tmem + lane_off + 256 + half * 128;
-    int n0 = 0, used = 0, done = 0;
+    int n0 = 0, used = 0, done = 0, turn = 0;   // turn: steps that both halves have taken part in
     for (int k = 0;; ++k) {
       const TqPiece walk = told(k);
       if (!walk.more) break;
       const int n1 = n0 + ((walk.b1 - walk.b0 + 1) >> 1);
       const int rr = walk.mt * TQ_ROWS + half * 128 + row;
-      const bool live = rr < walk.rows, takes_part = half == 0 || walk.rows > walk.mt * TQ_ROWS + 128;
+      const bool live = rr < walk.rows, both = walk.rows > walk.mt * TQ_ROWS + 128, takes_part = half == 0 || both;
       if (walk.b0 == walk.b1) {   // nothing to see: no other role takes part
         if (live) {
           const float zero[4] = {0.f, 0.f, 0.f, 0.f};
@@ -516,7 +523,10 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
         // R + 64 (P could pass its range): x is first written over S and its maximum found, R moves up to it if
         // need be, and the maximum less itself is zero however large it is.
         bool careful = __any_sync(0xffffffffu, see < 128 || R == -INFINITY || fabsf(R) > 4096.f) || ok != 3;
-        bool plain = true;
+        bool plain = true, passed = false;
+        // The halves take turns, so that one's pass runs beside the other's products; the turn is passed on after five
+        // of eight chunks (at the end: 716 us for the chunk of 4608 tokens, here 683, without turns 701).
+        if (both && (half == 1 || turn > 0)) wait(T_TURN + (half ^ 1), (half == 1 ? turn : turn - 1) & 1);
 #pragma unroll 1
         while (true) {
           if (careful && plain) {
@@ -554,13 +564,25 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
           f32x2 sum0 = 0ull, sum1 = 0ull;
           uint32_t x[2][16];
           tmem_ld16(tS, x[0]);
+          uint4 sc[2][2];
+          sc[0][0] = s8[0];
+          sc[0][1] = s8[1];
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
-            tmem_wait_ld();
-            if (q < 7) tmem_ld16(tS + (q + 1) * 16, x[(q + 1) & 1]);   // in flight behind this chunk
+            if (q == 5 && both && !passed) {
+              passed = true;
+              mbar_arrive(&bars[T_TURN + half]);
+              ++turn;
+            }
+            tmem_wait16(x[q & 1]);
+            if (q < 7) {
+              tmem_ld16(tS + (q + 1) * 16, x[(q + 1) & 1]);   // in flight behind this chunk
+              sc[(q + 1) & 1][0] = s8[q * 2 + 2];
+              sc[(q + 1) & 1][1] = s8[q * 2 + 3];
+            }
 #pragma unroll
             for (int e = 0; e < 16; e += 8) {
-              const uint4 s = s8[q * 2 + e / 8];
+              const uint4 s = sc[q & 1][e / 8];
               const uint32_t sw[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
@@ -656,6 +678,12 @@ cudaError_t launch_t(AttendQ4Params p, cudaStream_t st) {
   auto kern = attend_q4_tc_kernel<D>;
   cudaError_t e = set_smem_once((const void*)kern, (int)TqSmem<D>::BYTES);
   if (e != cudaSuccess) return e;
+  // setmaxnreg draws on the registers of the launch: fewer than the split asks for would be waited for without end
+  static const int regs = [] {
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, attend_q4_tc_kernel<D>) == cudaSuccess ? a.numRegs : 0;
+  }();
+  if (regs * 5 < (int)(REG_CTRL + 2 * REG_UNPACK + 2 * REG_SOFT)) return cudaErrorNotSupported;
   p.part_rows = TQ_ROWS;
   int sms = 0, dev = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
