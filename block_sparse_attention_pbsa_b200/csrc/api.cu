@@ -378,7 +378,7 @@ pbsa_status pbsa_request_tables(const int* step_len, const int* seq_len, int n_r
       free_cnt == nullptr || q_start == nullptr || q_len == nullptr || kv_len == nullptr || free_cnt_out == nullptr)
     return PBSA_ERR_INVALID_ARG;
   if (n_requests <= 0 || table_ld <= 0 || pool_slots <= 0 || n_tokens < 0) return PBSA_ERR_INVALID_ARG;
-  if (n_tokens > 0 && slot_map == nullptr) return PBSA_ERR_INVALID_ARG;
+  if ((n_tokens > 0 && slot_map == nullptr) || !aligned16(ws)) return PBSA_ERR_INVALID_ARG;
   if ((int64_t)pool_slots * BT >= ((int64_t)1 << 31) || (int64_t)table_ld * BT >= ((int64_t)1 << 31))
     return PBSA_ERR_INVALID_ARG;
   if (n_requests > 8192 || n_tokens > (1 << 28)) return PBSA_ERR_UNSUPPORTED;
@@ -391,7 +391,8 @@ pbsa_status pbsa_append_q4(const pbsa_req_geom* g, const void* k, long long k_ld
                            int n_tokens, const int* slot_map, void* pool, int pool_slots, void* ws, void* stream) {
   const pbsa_status s = check_req(g);
   if (s != PBSA_OK) return s;
-  if (n_tokens < 0 || pool == nullptr || !aligned16(pool) || !q4_pool_ok(g, pool_slots)) return PBSA_ERR_INVALID_ARG;
+  if (n_tokens < 0 || pool == nullptr || !aligned16(pool) || !aligned16(ws) || !q4_pool_ok(g, pool_slots))
+    return PBSA_ERR_INVALID_ARG;
   if (n_tokens == 0) return PBSA_OK;
   if (k == nullptr || v == nullptr || slot_map == nullptr || !aligned16(k) || !aligned16(v)) return PBSA_ERR_INVALID_ARG;
   const long long token = (long long)g->kv_heads * g->head_dim;
@@ -404,7 +405,8 @@ pbsa_status pbsa_expand_q4(const pbsa_req_geom* g, const void* pool, int pool_sl
                            void* k_pool, void* v_pool, void* ws, void* stream) {
   const pbsa_status s = check_req(g);
   if (s != PBSA_OK) return s;
-  if (n_slots < 0 || pool == nullptr || !aligned16(pool) || !q4_pool_ok(g, pool_slots)) return PBSA_ERR_INVALID_ARG;
+  if (n_slots < 0 || pool == nullptr || !aligned16(pool) || !aligned16(ws) || !q4_pool_ok(g, pool_slots))
+    return PBSA_ERR_INVALID_ARG;
   if (n_slots == 0) return PBSA_OK;
   if (src_slot == nullptr || k_pool == nullptr || v_pool == nullptr || !aligned16(k_pool) || !aligned16(v_pool))
     return PBSA_ERR_INVALID_ARG;

@@ -679,11 +679,9 @@ cudaError_t launch_t(AttendQ4Params p, cudaStream_t st) {
   cudaError_t e = set_smem_once((const void*)kern, (int)TqSmem<D>::BYTES);
   if (e != cudaSuccess) return e;
   // setmaxnreg draws on the registers of the launch: fewer than the split asks for would be waited for without end
-  static const int regs = [] {
-    cudaFuncAttributes a;
-    return cudaFuncGetAttributes(&a, attend_q4_tc_kernel<D>) == cudaSuccess ? a.numRegs : 0;
-  }();
-  if (regs * 5 < (int)(REG_CTRL + 2 * REG_UNPACK + 2 * REG_SOFT)) return cudaErrorNotSupported;
+  cudaFuncAttributes attr;
+  if ((e = cudaFuncGetAttributes(&attr, kern)) != cudaSuccess) return e;
+  if (attr.numRegs * 5 < (int)(REG_CTRL + 2 * REG_UNPACK + 2 * REG_SOFT)) return cudaErrorNotSupported;
   p.part_rows = TQ_ROWS;
   int sms = 0, dev = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;

@@ -13,6 +13,7 @@ step (or a step of every layer) can be captured in a CUDA graph and replayed whi
 """
 from __future__ import annotations
 
+import contextlib
 import dataclasses
 
 import torch
@@ -28,6 +29,11 @@ class RequestConfig:
     blocks: int
     tokens: int
     pool_slots: int
+
+
+def _on(stream):
+    """The context in which a call makes its own tensors: the stream that its kernels run on."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 class RequestBatch:
@@ -61,11 +67,8 @@ class RequestBatch:
         if step_len is not None and step_len is not self.step_len:
             if step_len.shape != self.step_len.shape:
                 raise ValueError(f"step_len must have {self.cfg.requests} entries, got {list(step_len.shape)}")
-            if stream is None:
+            with _on(stream):
                 self.step_len.copy_(step_len)
-            else:
-                with torch.cuda.stream(stream):
-                    self.step_len.copy_(step_len)
         self.max_q_len = max_q_len
         L.pbsa_request_tables(self.step_len, self.kv_len, self.block_table, self.free_slot, self.free_cnt, self.q_start,
                               self.q_len, self.kv_len, self.free_cnt, self.slot_map, self.position, ws=self.ws,
@@ -94,10 +97,11 @@ class Q4LayerCache:
 
     def __init__(self, batch: RequestBatch, q_heads: int, kv_heads: int, head_dim: int, dtype="bf16", scale=None, ws=None):
         self.batch = batch
-        self.geom = L.make_req_geom(q_heads, kv_heads, head_dim, scale or head_dim ** -0.5, dtype)
+        self.geom = L.make_req_geom(q_heads, kv_heads, head_dim, head_dim ** -0.5 if scale is None else scale,
+                                    dtype)
         block = L.pbsa_q4_block_bytes(self.geom)
         if block == 0:
-            raise ValueError("heads, head size or type that the 4-bit cache is not built for")
+            raise ValueError("heads, head size, scale or type that the 4-bit cache is not built for")
         self.pool = torch.zeros((kv_heads, batch.cfg.pool_slots, block), dtype=torch.uint8, device=batch.device)
         need = L.pbsa_attend_q4_workspace_bytes(self.geom)
         if ws is not None and ws.numel() * ws.element_size() < need:
@@ -123,7 +127,8 @@ class Q4LayerCache:
         if q.shape[0] != b.cfg.tokens:
             raise ValueError(f"a step has {b.cfg.tokens} token rows, got {q.shape[0]}")
         if o is None:
-            o = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+            with _on(stream):
+                o = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
         L.pbsa_attend_q4(self.geom, q, b.q_start, b.q_len, b.kv_len, b.max_q_len, self.pool, b.cfg.pool_slots,
                          b.block_table, causal, o, lse, ws=self.ws, stream=stream)
         return o
@@ -134,7 +139,8 @@ class Q4LayerCache:
         if k_pool is None or v_pool is None:
             dt = torch.bfloat16 if self.geom.dtype == L.PBSA_BF16 else torch.float32
             shape = (self.geom.kv_heads, slots.numel(), 64, self.geom.head_dim)
-            k_pool = torch.zeros(shape, dtype=dt, device=self.batch.device) if k_pool is None else k_pool
-            v_pool = torch.zeros(shape, dtype=dt, device=self.batch.device) if v_pool is None else v_pool
+            with _on(stream):
+                k_pool = torch.zeros(shape, dtype=dt, device=self.batch.device) if k_pool is None else k_pool
+                v_pool = torch.zeros(shape, dtype=dt, device=self.batch.device) if v_pool is None else v_pool
         L.pbsa_expand_q4(self.geom, self.pool, self.batch.cfg.pool_slots, slots, k_pool, v_pool, ws=self.ws, stream=stream)
         return k_pool, v_pool

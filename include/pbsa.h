@@ -340,7 +340,8 @@ PBSA_API pbsa_status pbsa_memory_update_noalloc(const pbsa_geom* g, const float*
  * ((max x - m) / 15 and (x_i - m) / s are fp32 products with the fp32 1/15 and 1/s).  A token whose K
  * or V of a head holds a value that is not finite, or a range above fp32's or bf16's, has NaN as that
  * head's K and zero as its V: queries that attend it yield NaN, others are not touched by it.
- * The fields' order inside a slot is the library's own: pbsa_expand_q4 reads it back.
+ * The fields' order inside a slot is the library's own: pbsa_append_q4 alone writes it, pbsa_expand_q4
+ * reads it back.  Workspaces are 16-byte aligned where they are given.
  *
  * A step of the requests: pbsa_request_tables once, then per layer pbsa_append_q4 of the step's K
  * and V and pbsa_attend_q4 of its Q.  Nothing needs the lengths on the host, so a captured step
@@ -412,7 +413,8 @@ PBSA_API pbsa_status pbsa_expand_q4(const pbsa_req_geom* g, const void* pool, in
  *  q      [n_tokens][q_heads][d] with q_ld elements between tokens; request r's rows are q_start[r] ..
  *         q_start[r] + q_len[r] - 1.  Rows of no request are neither read nor written.
  *  q_start, q_len, kv_len [n_requests] (n_requests <= 8192), on the device; max_q_len: no q_len is larger.
- *  block_table [n_requests][table_ld];  o like q, with o_ld;  lse nullable out [q_heads][n_tokens].
+ *  block_table [n_requests][table_ld];  o like q, with o_ld, and apart from it;
+ *  lse nullable out [q_heads][n_tokens].
  *  flags  0 or PBSA_CAUSAL.
  * A request whose numbers lie out of range (q_len > max_q_len, rows outside q, kv_len > 64 table_ld) is
  * left out and recorded; a slot outside the pool is recorded and its tokens are left out of the sums.

@@ -279,6 +279,12 @@ def test_long_cache_is_split_and_joined():
         f.check(*f.attend(True), True)
 
 
+@pytest.mark.parametrize("lens", [[(1, i % 3) for i in range(8192)], [(0, 1)] * 8190 + [(60, 70), (1, 64)]])
+def test_the_most_requests(lens):
+    f = Filled(lens, 1, 1, 64, "bf16", seed=17)
+    f.check(*f.attend(True), True)
+
+
 def test_rows_without_keys():
     """More step tokens than cached ones: the causal rule leaves the first rows no key; and no cache at all."""
     f = Filled([(5, 0), (4, 3)], 4, 2, 128, "bf16", seed=7)

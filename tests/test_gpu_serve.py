@@ -181,6 +181,24 @@ def test_a_stream_argument_is_used():
     assert torch.equal(o, want)
 
 
+def test_outputs_made_by_a_call_belong_to_its_stream():
+    """Outputs that attend and blocks make are cleared on the stream given, not on a current one that lags behind."""
+    batch = P.RequestBatch(P.RequestConfig(requests=1, blocks=2, tokens=70, pool_slots=2))
+    cache = P.Q4LayerCache(batch, 4, 2, 128)
+    gen = torch.Generator().manual_seed(6)
+    q, k, v = (torch.randn((70, h, 128), generator=gen).to(torch.bfloat16).to(DEV) for h in (4, 2, 2))
+    batch.step([70], 70)
+    cache.append(k, v)
+    slots = torch.tensor([0, 1], dtype=torch.int32, device=DEV)
+    want, (wk, wv) = cache.attend(q), cache.blocks(slots)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    torch.cuda._sleep(20_000_000)
+    o, (kp, vp) = cache.attend(q, stream=st), cache.blocks(slots, stream=st)
+    torch.cuda.synchronize()
+    assert torch.equal(o, want) and torch.equal(kp, wk) and torch.equal(vp, wv)
+
+
 def test_expanded_blocks_feed_the_block_attention():
     """4-bit blocks expanded into pools and attended by pbsa_attend: the result over the held values."""
     batch = P.RequestBatch(P.RequestConfig(requests=2, blocks=8, tokens=300, pool_slots=10))

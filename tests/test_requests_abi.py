@@ -117,3 +117,19 @@ def test_batch_refusals_on_the_host():
         c.append(torch.zeros(9, 2, 64), torch.zeros(9, 2, 64))
     with pytest.raises(ValueError):
         c.attend(torch.zeros(9, 2, 64))
+
+
+@host_only
+def test_misaligned_workspaces_are_refused(L):
+    f, m = 0x10000, 0x10004      # aligned / misaligned, never dereferenced
+    g = P.make_req_geom(32, 8, 128, 0.1, "bf16")
+    assert L.pbsa_request_tables(f, f, 4, f, 8, f, f, 100, 16, f, f, f, f, f, None, m, None) == 1
+    assert L.pbsa_append_q4(g, f, 1024, f, 1024, 4, f, f, 100, m, None) == 1
+    assert L.pbsa_expand_q4(g, f, 100, f, 4, f, f, m, None) == 1
+
+
+@host_only
+def test_a_scale_of_zero_is_refused(L):
+    batch = P.RequestBatch(P.RequestConfig(requests=1, blocks=1, tokens=1, pool_slots=1), device="cpu")
+    with pytest.raises(ValueError, match="scale"):
+        P.Q4LayerCache(batch, 2, 2, 64, scale=0.0)
