@@ -40,6 +40,7 @@ constexpr int AQ_WARPS = 4;                       // computing warps
 constexpr int AQ_THREADS = (AQ_WARPS + 1) * 32;   // + the producer
 constexpr int AQ_STAGES = 3;                      // of two slots each
 constexpr int AQ_MIN_STEPS = 4;                   // blocks that are worth a CTA of their own
+constexpr int AQ_TILE_COST = 3;                   // blocks that a tile's start and end take the time of
 
 template <int D, int NT>
 struct AqSmem {
@@ -100,7 +101,7 @@ __global__ void __launch_bounds__(AQ_THREADS, NT == 1 && SPLIT == 1 ? 3 : 2) att
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const Q4Share share = q4_share<AQ_THREADS>(p, ROWS, AQ_MIN_STEPS, &start_s);   // has block barriers
-  Q4Walk walk(p, share, ROWS);
+  Q4Walk walk(p, share, start_s, ROWS);
 
   if (warp == AQ_WARPS) {
     // ------------------------------------------------------------- producer
@@ -426,6 +427,7 @@ cudaError_t launch_t(AttendQ4Params p, cudaStream_t st) {
   cudaError_t e = set_smem_once((const void*)kern, smem);
   if (e != cudaSuccess) return e;
   p.part_rows = AqSmem<D, NT>::ROWS;
+  p.tile_cost = AQ_TILE_COST;
   const int per_sm = NT == 1 && SPLIT == 1 ? 3 : 2;
   int sms = 0, dev = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;

@@ -36,6 +36,7 @@ struct AttendQ4Params {
   int f32;
   int rows_above, rows_to;   // this kernel's requests have rows_above < q_len * group <= rows_to
   int part_rows;             // rows of a piece in the workspace
+  int tile_cost;             // blocks that a tile is charged beside its own
   Q4Desc* desc;
   float2* part_ml;           // (reference maximum in log2 units, sum) of a piece's row
   float* part_o;
@@ -77,7 +78,12 @@ struct Q4Request {
 
   __device__ long long charged_to(int n) const {   // the first n tiles
     if (base < 0) return (long long)n * blocks;
-    return n == 0 ? 0 : (long long)n * base + floor_sum(n, den, num, num + den - 1);
+    if (n == 0) return 0;
+    if ((uint32_t)den % (uint32_t)num == 0) {      // sum of ceil(k / per): whole groups of `per` tiles, and the rest
+      const int per = (uint32_t)den / (uint32_t)num, whole = (uint32_t)n / (uint32_t)per, rest = n - whole * per;
+      return (long long)n * base + ((long long)whole * (whole + 1) / 2 * per + (long long)rest * (whole + 1));
+    }
+    return (long long)n * base + floor_sum(n, den, num, num + den - 1);
   }
   __device__ int charge(int mt) const {
     return base < 0 ? blocks : base + (int)quotient((long long)num * (mt + 1) + den - 1, den);
@@ -104,22 +110,22 @@ __device__ __forceinline__ Q4Request q4_request(const AttendQ4Params& p, int r, 
   const int rows = x.q_len * p.group;
   if (rows <= p.rows_above || rows > p.rows_to) return x;   // the other kernel's
   x.tiles = (rows + tile_rows - 1) / tile_rows;
-  x.blocks = max(1, (x.kv_len + BT - 1) / BT);   // a request without keys has its rows written too
-  if (p.causal && x.tiles > 1) x.base = (max(x.kv_len - x.q_len, 0) + BT - 1) / BT;
+  x.blocks = p.tile_cost + max(1, (x.kv_len + BT - 1) / BT);   // a request without keys has its rows written too
+  if (p.causal && x.tiles > 1) x.base = p.tile_cost + (max(x.kv_len - x.q_len, 0) + BT - 1) / BT;
   return x;
 }
 
+// Where a CTA's share starts: the request, kv head, row tile, and the blocks of the tile that lie before.
 struct Q4Start {
-  int r;
-  long long off;     // place of the share's first step inside request r
+  Q4Request req;
+  int r, h, mt, at;
 };
 struct Q4Share {
   long long total, x0, x1;
-  int ctas, r;
-  long long off;
+  int ctas;
 };
 
-// This CTA's share [x0, x1) of the line, and the request it starts in.  Every thread calls it.
+// This CTA's share [x0, x1) of the line, and its start in shared memory.  Every thread calls it.
 template <int THREADS>
 __device__ __forceinline__ Q4Share q4_share(const AttendQ4Params& p, int tile_rows, int min_steps, Q4Start* start) {
   __shared__ long long sums[THREADS / 32];
@@ -127,7 +133,11 @@ __device__ __forceinline__ Q4Share q4_share(const AttendQ4Params& p, int tile_ro
   const int per = (p.R + THREADS - 1) / THREADS;
   const int r0 = min(tid * per, p.R), r1 = min(r0 + per, p.R);
   long long mine = 0;
-  for (int r = r0; r < r1; ++r) mine += p.kv_heads * q4_request(p, r, tile_rows, blockIdx.x == 0).head_steps();
+  Q4Request req;
+  for (int r = r0; r < r1; ++r) {
+    req = q4_request(p, r, tile_rows, blockIdx.x == 0);
+    mine += p.kv_heads * req.head_steps();
+  }
   long long upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -154,21 +164,30 @@ __device__ __forceinline__ Q4Share q4_share(const AttendQ4Params& p, int tile_ro
     s.x0 = whole * blockIdx.x + rest * blockIdx.x / (uint32_t)s.ctas;
     s.x1 = whole * (blockIdx.x + 1) + rest * (blockIdx.x + 1) / (uint32_t)s.ctas;
     long long at = before + upto - mine;
-    if (s.x0 >= at && s.x0 < at + mine) {
-      for (int r = r0; r < r1; ++r) {
-        const long long n = p.kv_heads * q4_request(p, r, tile_rows, false).head_steps();
-        if (s.x0 < at + n) {
-          start->r = r;
-          start->off = s.x0 - at;
-          break;
-        }
+    if (s.x0 >= at && s.x0 < at + mine) {   // one thread
+      int r = r0;
+      for (;; ++r) {
+        if (per > 1) req = q4_request(p, r, tile_rows, false);
+        const long long n = p.kv_heads * req.head_steps();
+        if (s.x0 < at + n) break;
         at += n;
       }
+      const long long head = req.head_steps();
+      start->h = (int)quotient(s.x0 - at, head);
+      const long long off = s.x0 - at - start->h * head;
+      int lo = 0, hi = req.tiles - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (req.charged_to(mid) <= off) lo = mid;
+        else hi = mid - 1;
+      }
+      start->req = req;
+      start->r = r;
+      start->mt = lo;
+      start->at = (int)(off - req.charged_to(lo));
     }
   }
   __syncthreads();
-  s.r = start->r;
-  s.off = start->off;
   return s;
 }
 
@@ -185,23 +204,15 @@ struct Q4Walk {
   int piece;      // its place in the workspace; -1: the whole tile
   Q4Desc desc;    // the tile that goes on in a later CTA
 
-  __device__ Q4Walk(const AttendQ4Params& prm, const Q4Share& s, int tr)
-      : p(prm), x(s.x0), x1(s.x1), total(s.total), ctas(s.ctas), tile_rows(tr), r(s.r) {
+  __device__ Q4Walk(const AttendQ4Params& prm, const Q4Share& s, const Q4Start& start, int tr)
+      : p(prm), x(s.x0), x1(s.x1), total(s.total), ctas(s.ctas), tile_rows(tr) {
     desc.pieces = 0;
     if (x >= x1) return;
-    // the head and row tile of the share's first step
-    req = q4_request(p, r, tile_rows, false);
-    const long long head = req.head_steps();
-    h = (int)quotient(s.off, head);
-    const long long off = s.off - h * head;
-    int lo = 0, hi = req.tiles - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (req.charged_to(mid) <= off) lo = mid;
-      else hi = mid - 1;
-    }
-    mt = lo;
-    at = (int)(off - req.charged_to(mt));
+    req = start.req;
+    r = start.r;
+    h = start.h;
+    mt = start.mt;
+    at = start.at;
     charge = req.charge(mt);
   }
 

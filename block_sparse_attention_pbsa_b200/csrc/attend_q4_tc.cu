@@ -40,6 +40,7 @@ namespace {
 constexpr int TQ_THREADS = 640;      // warpgroups: control, unpack x 2, softmax x 2
 constexpr int TQ_ROWS = 256;         // two halves of 128
 constexpr int TQ_MIN_STEPS = 8;      // blocks that are worth a CTA of their own
+constexpr int TQ_TILE_COST = 12;     // blocks that a tile's start and end and its two passes over masked steps cost
 constexpr int STAGES = 2, SCS = 4;   // operand stages of K and of V, key scales
 constexpr uint32_t REG_CTRL = 48, REG_UNPACK = 80, REG_SOFT = 136;   // launched with 96: 48 + 2*80 + 2*136 = 5*96
 static_assert(REG_CTRL + 2 * REG_UNPACK + 2 * REG_SOFT <= 5 * 96, "register split exceeds the launch");
@@ -194,7 +195,7 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
     if (warp == 2) {
       // ------------------------------------------------------------- walks the share
       if (lane == 0) {
-        Q4Walk walk(p, share, TQ_ROWS);
+        Q4Walk walk(p, share, start_s, TQ_ROWS);
         bool more = true;
         for (int k = 0; more; ++k) {
           more = walk.next();
@@ -683,6 +684,7 @@ cudaError_t launch_t(AttendQ4Params p, cudaStream_t st) {
   if ((e = cudaFuncGetAttributes(&attr, kern)) != cudaSuccess) return e;
   if (attr.numRegs * 5 < (int)(REG_CTRL + 2 * REG_UNPACK + 2 * REG_SOFT)) return cudaErrorNotSupported;
   p.part_rows = TQ_ROWS;
+  p.tile_cost = TQ_TILE_COST;
   int sms = 0, dev = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
