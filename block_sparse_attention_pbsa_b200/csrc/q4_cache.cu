@@ -1,8 +1,8 @@
 // Tokens into the 4-bit cache (append) and blocks of it back into dense block pools (expand).
 //
 // append: for token t with slot_map[t] = slot*64 + row >= 0 and each head, the K and V vectors are
-// quantised as q4.cuh defines and written to (head, slot, row).  One thread holds 8 neighbouring
-// channels (one or two 16-byte loads); the 16 (D = 64: 8) threads of a vector find its minimum and
+// quantised as q4.cuh defines and written to (head, slot, row).  One thread holds 16 neighbouring
+// channels (two or four 16-byte loads); the 8 (D = 64: 4) threads of a vector find its minimum and
 // maximum by shuffles, and a warp holds the K and the V of a token and head together, so that a
 // token whose K or V is not finite can be marked as one: its K scale and minimum become NaN (every
 // query that attends it then yields NaN) and its V zero, which keeps NaN out of the rows that
@@ -10,7 +10,11 @@
 // expand: s*c + m of every token of the listed slots, rounded once to the pools' type, in the
 // layout of the block pools that pbsa_attend reads.
 //
-// Both are bound by HBM: append reads 2*D*sizeof(T) bytes and writes D + 8 per (token, head).
+// append reads 2*D*sizeof(T) bytes and writes D + 8 per (token, head): 36 MB, 5.5 us, for 4608 tokens of 12
+// heads, which take 10.1 us (3.6 TB/s).  It is bound by issue: about 130 warp instructions a token and head, most
+// of them per thread (range, scale, addresses), which is why a thread holds as many channels as one
+// group of V's layout.  With 8 channels a thread they were 216, and 15.2 us.
+// expand moves the same bytes the other way in 6.1 us (5.9 TB/s), bound by HBM.
 #include "internal.h"
 #include "q4.cuh"
 
@@ -27,29 +31,32 @@ struct AppendParams {
   void* ws;
 };
 
-// 8 neighbouring channels as they lie in memory.
+// 16 neighbouring channels as they lie in memory.
 template <typename T>
-struct Eight;
+struct Sixteen;
 template <>
-struct Eight<float> {
-  float4 a, b;
-  __device__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ void load(const float* p) {
-    a = __ldg(reinterpret_cast<const float4*>(p));
-    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+struct Sixteen<float> {
+  float4 a[4];
+  __device__ void zero() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  __device__ void values(float (&x)[8]) const {
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  __device__ void load(const float* p) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = __ldg(reinterpret_cast<const float4*>(p) + i);
+  }
+  __device__ void values(float (&x)[16]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { x[4 * i] = a[i].x; x[4 * i + 1] = a[i].y; x[4 * i + 2] = a[i].z; x[4 * i + 3] = a[i].w; }
   }
   // least and greatest of the vector that `N` neighbouring threads hold (NaN if any is)
   template <int N>
   __device__ void range(float& lo, float& hi) const {
-    float x[8];
+    float x[16];
     values(x);
     lo = hi = x[0];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) { lo = min_nan(lo, x[i]); hi = max_nan(hi, x[i]); }
+    for (int i = 1; i < 16; ++i) { lo = min_nan(lo, x[i]); hi = max_nan(hi, x[i]); }
 #pragma unroll
     for (int o = 1; o < N; o <<= 1) {
       lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
@@ -62,21 +69,29 @@ __device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
   asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 template <>
-struct Eight<__nv_bfloat16> {
-  uint4 a;
-  __device__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
-  __device__ void load(const __nv_bfloat16* p) { a = __ldg(reinterpret_cast<const uint4*>(p)); }
-  __device__ void values(float (&x)[8]) const {
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+struct Sixteen<__nv_bfloat16> {
+  uint4 a, b;
+  __device__ void zero() { a = b = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ void load(const __nv_bfloat16* p) {
+    a = __ldg(reinterpret_cast<const uint4*>(p));
+    b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+  }
+  __device__ void values(float (&x)[16]) const {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) { x[2 * i] = lo_bf16(w[i]); x[2 * i + 1] = hi_bf16(w[i]); }
+    for (int i = 0; i < 8; ++i) { x[2 * i] = lo_bf16(w[i]); x[2 * i + 1] = hi_bf16(w[i]); }
   }
   // as above, two at a time: (least, -greatest) travel as one pair of bf16, both taken by minima
   template <int N>
   __device__ void range(float& lo, float& hi) const {
-    const uint32_t least = min2_nan(min2_nan(a.x, a.y), min2_nan(a.z, a.w)), n = 0x80008000u;
-    const uint32_t most = min2_nan(min2_nan(a.x ^ n, a.y ^ n), min2_nan(a.z ^ n, a.w ^ n));
+    const uint32_t least = min2_nan(min2_nan(min2_nan(a.x, a.y), min2_nan(a.z, a.w)), min2_nan(min2_nan(b.x, b.y), min2_nan(b.z, b.w)));
+    const uint32_t most = max2_nan(max2_nan(max2_nan(a.x, a.y), max2_nan(a.z, a.w)), max2_nan(max2_nan(b.x, b.y), max2_nan(b.z, b.w))) ^ 0x80008000u;
     uint32_t r = min2_nan(__byte_perm(least, most, 0x5410), __byte_perm(least, most, 0x7632));
 #pragma unroll
     for (int o = 1; o < N; o <<= 1) r = min2_nan(r, __shfl_xor_sync(0xffffffffu, r, o));
@@ -92,13 +107,13 @@ __device__ __forceinline__ uint32_t four(uint32_t a, uint32_t b, uint32_t c, uin
   return a + 16u * b + 256u * c + 4096u * d - 4369u * 0x4B400000u;
 }
 
-constexpr int AP_THREADS = 256;
+constexpr int AP_THREADS = 64;   // (256: the 64 tokens of a decode step take 2.7 us instead of 2.3)
 
 // U neighbouring tokens of a head at once: their slots and then their values are in flight together, and the two
 // tokens that share V's words are mostly written as one
 template <typename T, int D, int U>
 __global__ void __launch_bounds__(AP_THREADS) append_q4_kernel(const AppendParams p) {
-  constexpr int LPV = D / 8;            // threads of a vector
+  constexpr int LPV = D / 16;            // threads of a vector
   constexpr int PAIRS = 32 / (2 * LPV);  // (token, head) pairs of a warp
   using Q = Q4<D>;
   const int lane = threadIdx.x & 31;
@@ -113,10 +128,10 @@ __global__ void __launch_bounds__(AP_THREADS) append_q4_kernel(const AppendParam
     const bool in = it < items;
     const int run = in ? (int)(it / p.H) : 0, h = in ? (int)(it - (long long)run * p.H) : 0;
     int at[U];
-    Eight<T> x[U];
+    Sixteen<T> x[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) at[u] = in && run * U + u < p.T ? __ldg(p.slot_map + run * U + u) : -1;
-    const T* src = static_cast<const T*>(part ? p.v : p.k) + (long long)run * U * (part ? p.v_ld : p.k_ld) + (long long)h * D + 8 * l;
+    const T* src = static_cast<const T*>(part ? p.v : p.k) + (long long)run * U * (part ? p.v_ld : p.k_ld) + (long long)h * D + 16 * l;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const bool ok = at[u] >= 0 && at[u] < p.pool_slots * BT;
@@ -127,11 +142,11 @@ __global__ void __launch_bounds__(AP_THREADS) append_q4_kernel(const AppendParam
       x[u].zero();
       if (ok) x[u].load(src + u * (part ? p.v_ld : p.k_ld));
     }
-    uint32_t lower[U], upper[U];   // K: a word's even and odd channels; V: channels 0 .. 3 and 4 .. 7
+    uint32_t code[U][4];   // K: even and odd channels of a word, then of the next; V: channels 0 .. 3, 4 .. 7, ...
     uint32_t sm[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      float lo, hi, v[8];
+      float lo, hi, v[16];
       x[u].template range<LPV>(lo, hi);
       x[u].values(v);
       const float m = bf16_down(lo);
@@ -145,14 +160,17 @@ __global__ void __launch_bounds__(AP_THREADS) append_q4_kernel(const AppendParam
       const bool poison = (votes & pair) != 0;
       const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
       // no code is above 15: s >= (hi - m) / 15 (1 - 2^-23), and 15.5 is far off
-      uint32_t c[8];
+      uint32_t c[16];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) c[i] = rounded_bits(__fmul_rn(__fsub_rn(v[i], m), inv));
-      lower[u] = part ? four(c[0], c[1], c[2], c[3]) : four(c[0], c[2], c[4], c[6]);
-      upper[u] = part ? four(c[4], c[5], c[6], c[7]) : four(c[1], c[3], c[5], c[7]);
+      for (int i = 0; i < 16; ++i) c[i] = rounded_bits(__fmul_rn(__fsub_rn(v[i], m), inv));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int e = 8 * (i >> 1) + (i & 1);
+        code[u][i] = part ? four(c[4 * i], c[4 * i + 1], c[4 * i + 2], c[4 * i + 3]) : four(c[e], c[e + 2], c[e + 4], c[e + 6]);
+      }
       sm[u] = (__float_as_uint(s) >> 16) | (__float_as_uint(m) & 0xFFFF0000u);
       if (poison) {
-        lower[u] = upper[u] = 0u;
+        code[u][0] = code[u][1] = code[u][2] = code[u][3] = 0u;
         sm[u] = part ? 0u : 0x7FC07FC0u;
       }
     }
@@ -163,18 +181,27 @@ __global__ void __launch_bounds__(AP_THREADS) append_q4_kernel(const AppendParam
       uint8_t* blk = p.pool + ((size_t)h * p.pool_slots + slot) * Q::BYTES;
       if (l == 0) *reinterpret_cast<uint32_t*>(blk + (part ? Q::OFF_VS : Q::OFF_KS) + 4 * row) = sm[u];
       if (part == 0) {
-        *reinterpret_cast<uint32_t*>(blk + row * Q::KROW + 4 * l) = lower[u] | upper[u] << 16;
+        *reinterpret_cast<uint2*>(blk + row * Q::KROW + 8 * l) =
+            make_uint2(code[u][0] | code[u][1] << 16, code[u][2] | code[u][3] << 16);
         continue;
       }
-      // 8 channels are half words of words (8l % (D/8)) / 4 and the next of group 8l / (D/8); the two tokens of a word
+      // 16 channels are half words of four words, in one group of D/8 channels or in two; the two tokens of a word
       // are written together where both are here
-      uint8_t* dst = blk + Q::OFF_V + Q::v_at(row, (8 * l) / (D / 8)) + ((8 * l) % (D / 8));
+      constexpr int GROUPS = 128 / D, PER = 4 / GROUPS;   // groups of the channels, words of each
+      uint8_t* dst = blk + Q::OFF_V + Q::v_at(row, l * GROUPS);
+      const uint32_t(&mine)[4] = code[u], (&next)[4] = code[u + 1 < U ? u + 1 : u];
       if (u + 1 < U && (row & 1) == 0 && at[u + 1 < U ? u + 1 : u] == at[u] + 1) {
-        *reinterpret_cast<uint32_t*>(dst) = lower[u] | lower[u + 1 < U ? u + 1 : u] << 16;
-        *reinterpret_cast<uint32_t*>(dst + 4) = upper[u] | upper[u + 1 < U ? u + 1 : u] << 16;
+        if (GROUPS == 1) {
+          *reinterpret_cast<uint4*>(dst) = make_uint4(mine[0] | next[0] << 16, mine[1] | next[1] << 16, mine[2] | next[2] << 16,
+                                                      mine[3] | next[3] << 16);
+        } else {
+          *reinterpret_cast<uint2*>(dst) = make_uint2(mine[0] | next[0] << 16, mine[1] | next[1] << 16);
+          *reinterpret_cast<uint2*>(dst + 4 * Q::LANE) = make_uint2(mine[2] | next[2] << 16, mine[3] | next[3] << 16);
+        }
       } else if (u == 0 || (row & 1) == 0 || at[u > 0 ? u - 1 : 0] != at[u] - 1) {
-        *reinterpret_cast<uint16_t*>(dst) = (uint16_t)lower[u];
-        *reinterpret_cast<uint16_t*>(dst + 4) = (uint16_t)upper[u];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint16_t*>(dst + i / PER * 4 * Q::LANE + i % PER * 4) = (uint16_t)mine[i];
       }
     }
   }
@@ -249,17 +276,17 @@ __global__ void __launch_bounds__(EX_THREADS) expand_q4_kernel(const ExpandParam
 
 template <typename T, int D, int U>
 cudaError_t append_u(const AppendParams& p, cudaStream_t st) {
-  constexpr int PAIRS = 32 / (D / 4);
+  constexpr int PAIRS = 32 / (D / 8);
   const long long warps = ((long long)((p.T + U - 1) / U) * p.H + PAIRS - 1) / PAIRS;
   const long long ctas = (warps + AP_THREADS / 32 - 1) / (AP_THREADS / 32);
-  append_q4_kernel<T, D, U><<<(unsigned)(ctas < 148 * 8 ? ctas : 148 * 8), AP_THREADS, 0, st>>>(p);
+  append_q4_kernel<T, D, U><<<(unsigned)(ctas < 148 * 32 ? ctas : 148 * 32), AP_THREADS, 0, st>>>(p);
   return cudaGetLastError();
 }
 
 template <typename T, int D>
 cudaError_t append_t(const AppendParams& p, cudaStream_t st) {
   // a few items are spread over warps, many are loaded four at a time
-  return (long long)p.T * p.H < 16384 ? append_u<T, D, 1>(p, st) : append_u<T, D, 4>(p, st);
+  return (long long)p.T * p.H < 16384 ? append_u<T, D, 1>(p, st) : append_u<T, D, 2>(p, st);
 }
 
 }  // namespace
