@@ -421,51 +421,60 @@ __global__ void __launch_bounds__(AQ_THREADS, NT == 1 && SPLIT == 1 ? 3 : 2) att
 }
 
 template <int D, int NT, int SPLIT>
-cudaError_t launch_t(AttendQ4Params p, cudaStream_t st) {
+cudaError_t launch_t(AttendQ4Params* p, int* grid, cudaStream_t st) {
   auto kern = attend_q4_kernel<D, NT, SPLIT>;
   constexpr int smem = AqSmem<D, NT>::TOTAL;
   cudaError_t e = set_smem_once((const void*)kern, smem);
   if (e != cudaSuccess) return e;
-  p.part_rows = AqSmem<D, NT>::ROWS;
-  p.tile_cost = AQ_TILE_COST;
+  p->part_rows = AqSmem<D, NT>::ROWS;
+  p->tile_cost = AQ_TILE_COST;
   const int per_sm = NT == 1 && SPLIT == 1 ? 3 : 2;
   int sms = 0, dev = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-  const int grid = sms * per_sm < Q4_MAX_CTAS ? sms * per_sm : Q4_MAX_CTAS;
-  kern<<<grid, AQ_THREADS, smem, st>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_q4_join<D>(p, grid, 1, st);
+  *grid = sms * per_sm < Q4_MAX_CTAS ? sms * per_sm : Q4_MAX_CTAS;
+  kern<<<*grid, AQ_THREADS, smem, st>>>(*p);
+  return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t launch_d(AttendQ4Params p, int dtype, int max_rows, cudaStream_t st) {
+  Q4JoinParams j = {};
+  // Requests of more than Q4_TC_ROWS rows fill enough of a 256-row tensor-core tile (attend_q4_tc.cu).
+  const bool many = dtype == PBSA_BF16 && max_rows > Q4_TC_ROWS;
   p.rows_above = 0;
-  if (dtype == PBSA_F32) {
+  p.rows_to = many ? Q4_TC_ROWS : max_rows;
+  cudaError_t e = dtype == PBSA_F32 ? launch_t<D, 1, 3>(&p, &j.few, st)
+                  : max_rows <= 8   ? launch_t<D, 1, 1>(&p, &j.few, st)
+                                    : launch_t<D, 2, 1>(&p, &j.few, st);
+  if (e != cudaSuccess) return e;
+  j.p = p;
+  if (many) {
+    // its pieces lie behind the others: the two kernels may run at the same time
+    p.rows_above = Q4_TC_ROWS;
     p.rows_to = max_rows;
-    return launch_t<D, 1, 3>(p, st);
+    j.tc_desc = p.desc += Q4_MAX_CTAS;
+    j.tc_ml = p.part_ml += Q4_FEW_ROWS;
+    j.tc_o = p.part_o += (size_t)Q4_FEW_ROWS * D;
+    if ((e = launch_attend_q4_tc(p, D, &j.tc, &j.tc_rows, st)) != cudaSuccess) return e;
   }
-  // Requests of more than Q4_TC_ROWS rows fill enough of a 128-row tensor-core tile (attend_q4_tc.cu).
-  p.rows_to = max_rows < Q4_TC_ROWS ? max_rows : Q4_TC_ROWS;
-  cudaError_t e = max_rows <= 8 ? launch_t<D, 1, 1>(p, st) : launch_t<D, 2, 1>(p, st);
-  if (e != cudaSuccess || max_rows <= Q4_TC_ROWS) return e;
-  p.rows_above = Q4_TC_ROWS;
-  p.rows_to = max_rows;
-  return launch_attend_q4_tc(p, D, st);
+  cudaLaunchAttribute late;
+  const cudaLaunchConfig_t cfg = q4_dependent(j.few + 4 * j.tc, 256, 0, st, &late);
+  return cudaLaunchKernelEx(&cfg, attend_q4_join_kernel<D>, j);
 }
 
 }  // namespace
 
 size_t attend_q4_ws_bytes(int d) {
   // descriptors, then the sums and the rows of two pieces a CTA
-  return (size_t)WS_HEADER_BYTES + Q4_MAX_CTAS * sizeof(Q4Desc) + (size_t)Q4_PART_ROWS * (8 + 4 * (size_t)d);
+  return (size_t)WS_HEADER_BYTES + (Q4_MAX_CTAS + Q4_TC_MAX_CTAS) * sizeof(Q4Desc) + (size_t)Q4_PART_ROWS * (8 + 4 * (size_t)d);
 }
 
 cudaError_t launch_attend_q4(const AttendQ4Params& in, int d, int dtype, int max_rows, cudaStream_t st) {
   AttendQ4Params p = in;
   uint8_t* w = static_cast<uint8_t*>(p.ws) + WS_HEADER_BYTES;
   p.desc = reinterpret_cast<Q4Desc*>(w);
-  w += Q4_MAX_CTAS * sizeof(Q4Desc);
+  w += (Q4_MAX_CTAS + Q4_TC_MAX_CTAS) * sizeof(Q4Desc);
   p.part_ml = reinterpret_cast<float2*>(w);
   w += (size_t)Q4_PART_ROWS * sizeof(float2);
   p.part_o = reinterpret_cast<float*>(w);

@@ -8,10 +8,10 @@
 
 namespace pbsa {
 
-constexpr int Q4_MAX_CTAS = 640;      // of a grid of the few-rows kernel (16 rows a piece)
+constexpr int Q4_MAX_CTAS = 480;      // of a grid of the few-rows kernel (16 rows a piece)
 constexpr int Q4_TC_MAX_CTAS = 160;   // of a grid of the tensor-core kernel (256 rows a piece)
-constexpr int Q4_PART_ROWS = 2 * (Q4_MAX_CTAS * 16 > Q4_TC_MAX_CTAS * 256 ? Q4_MAX_CTAS * 16 : Q4_TC_MAX_CTAS * 256);
-constexpr int Q4_TC_ROWS = 48;        // requests with more rows go to the tensor-core kernel
+constexpr int Q4_FEW_ROWS = 2 * Q4_MAX_CTAS * 16, Q4_PART_ROWS = Q4_FEW_ROWS + 2 * Q4_TC_MAX_CTAS * 256;   // of all pieces
+constexpr int Q4_TC_ROWS = 80;        // requests with more rows go to the tensor-core kernel
 
 // A tile that starts in this CTA and ends in a later one (pieces = 0: none).
 struct __align__(8) Q4Desc {
@@ -286,68 +286,107 @@ __device__ __forceinline__ void q4_write_row(const AttendQ4Params& p, int q0, in
     p.lse[(size_t)head * p.T + q0 + tok] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
 }
 
-// Joins the pieces of the tile that starts in CTA blockIdx.x and ends in a later one.
+// Four channels of a row of the tile that starts in CTA `cta` and ends in a later one: its pieces joined, in order.
 template <int D>
-__global__ void __launch_bounds__(256) attend_q4_join_kernel(const AttendQ4Params p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Q4Desc d = p.desc[blockIdx.x];
-  if (d.pieces == 0) return;
-  constexpr int CH = D / 4, RPP = 256 / CH;
-  const int ch = threadIdx.x % CH;
-  auto at = [&](int k) { return (size_t)(k == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + k)) * p.part_rows; };
-  for (int r = threadIdx.x / CH + RPP * blockIdx.y; r < d.rows; r += RPP * gridDim.y) {
-    // 8 pieces at a time, their loads in flight together (a place past the end repeats the last piece, unused)
-    float M = -INFINITY, L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+__device__ __forceinline__ void q4_join_row(const AttendQ4Params& p, const Q4Desc& d, int cta, const float2* part_ml,
+                                            const float* part_o, int part_rows, int r, int ch) {
+  auto at = [&](int k) { return (size_t)(k == 0 ? 2 * cta + 1 : 2 * (cta + k)) * part_rows; };
+  // 8 pieces at a time, their loads in flight together (a place past the end repeats the last piece, unused)
+  float M = -INFINITY, L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-    for (int k0 = 0; k0 < d.pieces; k0 += 8) {
-      float2 ml[8];
-      float4 v[8];
+  for (int k0 = 0; k0 < d.pieces; k0 += 8) {
+    float2 ml[8];
+    float4 v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const size_t place = at(min(k0 + i, d.pieces - 1)) + r;
-        ml[i] = p.part_ml[place];
-        v[i] = *reinterpret_cast<const float4*>(p.part_o + place * D + 4 * ch);
-      }
-      float top = M;
+    for (int i = 0; i < 8; ++i) {
+      const size_t place = at(min(k0 + i, d.pieces - 1)) + r;
+      ml[i] = part_ml[place];
+      v[i] = *reinterpret_cast<const float4*>(part_o + place * D + 4 * ch);
+    }
+    float top = M;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) top = fmaxf(top, ml[i].x);
-      const float f0 = M == top ? 1.f : q4_weight(M, top);
-      M = top;
-      L *= f0;
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, ml[i].x);
+    const float f0 = M == top ? 1.f : q4_weight(M, top);
+    M = top;
+    L *= f0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[e] *= f0;
+    for (int e = 0; e < 4; ++e) acc[e] *= f0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (k0 + i < d.pieces) {
-          const float f = q4_weight(ml[i].x, M);
-          L = fmaf(f, ml[i].y, L);
-          acc[0] = fmaf(f, v[i].x, acc[0]);
-          acc[1] = fmaf(f, v[i].y, acc[1]);
-          acc[2] = fmaf(f, v[i].z, acc[2]);
-          acc[3] = fmaf(f, v[i].w, acc[3]);
-        }
+    for (int i = 0; i < 8; ++i) {
+      if (k0 + i < d.pieces) {
+        const float f = q4_weight(ml[i].x, M);
+        L = fmaf(f, ml[i].y, L);
+        acc[0] = fmaf(f, v[i].x, acc[0]);
+        acc[1] = fmaf(f, v[i].y, acc[1]);
+        acc[2] = fmaf(f, v[i].z, acc[2]);
+        acc[3] = fmaf(f, v[i].w, acc[3]);
       }
     }
-    q4_write_row<D>(p, d.q0, d.row0 + r, d.h, 4 * ch, acc, M, L, ch == 0);
+  }
+  q4_write_row<D>(p, d.q0, d.row0 + r, d.h, 4 * ch, acc, M, L, ch == 0);
+}
+
+// Joins the pieces of both kernels.  The first `few` CTAs take a tile of the few-rows kernel each.  The others list the
+// tensor-core kernel's tiles (each for itself) and share their rows, 8 at a time: there may be one tile of a hundred
+// pieces or a hundred tiles of two.  (With 8 CTAs for each tile, 64 tokens of 8 heads over 30000 took 80 us, like this
+// 54; such a list of the few-rows kernel's tiles would cost single tokens 0.8 us.)
+struct Q4JoinParams {
+  AttendQ4Params p;          // descriptors and pieces are the few-rows kernel's
+  const Q4Desc* tc_desc;     // ... and these the tensor-core kernel's
+  const float2* tc_ml;
+  const float* tc_o;
+  int tc_rows, few, tc;      // CTAs of either
+};
+
+template <int D>
+__global__ void __launch_bounds__(256) attend_q4_join_kernel(const Q4JoinParams jp) {
+  __shared__ int counts[8], list[Q4_TC_MAX_CTAS];
+  constexpr int CH = D / 4, RPP = 256 / CH, PARTS = 256 / RPP;
+  const int tid = threadIdx.x, ch = tid % CH;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if ((int)blockIdx.x < jp.few) {
+    const Q4Desc d = jp.p.desc[blockIdx.x];
+    if (d.pieces == 0) return;
+    for (int r = tid / CH; r < d.rows; r += RPP)
+      q4_join_row<D>(jp.p, d, blockIdx.x, jp.p.part_ml, jp.p.part_o, jp.p.part_rows, r, ch);
+    return;
+  }
+  // the same list in every CTA: in the tiles' order
+  static_assert(Q4_TC_MAX_CTAS <= 256, "a thread a descriptor");
+  const bool mine = tid < jp.tc && jp.tc_desc[tid].pieces > 0;
+  const unsigned votes = __ballot_sync(0xffffffffu, mine);
+  if ((tid & 31) == 0) counts[tid >> 5] = __popc(votes);
+  __syncthreads();
+  int before = 0, count = 0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    if (w < (tid >> 5)) before += counts[w];
+    count += counts[w];
+  }
+  if (mine) list[before + __popc(votes & ((1u << (tid & 31)) - 1u))] = tid;
+  __syncthreads();
+  for (int item = blockIdx.x - jp.few; item < count * PARTS; item += gridDim.x - jp.few) {
+    const int cta = list[item / PARTS], r = item % PARTS * RPP + tid / CH;
+    const Q4Desc d = jp.tc_desc[cta];
+    if (r < d.rows) q4_join_row<D>(jp.p, d, cta, jp.tc_ml, jp.tc_o, jp.tc_rows, r, ch);
   }
 }
 
-// The join as a programmatic dependent of the attention kernel just launched: `grid` CTAs of that kernel,
-// `split` CTAs for the rows of each tile.
-template <int D>
-cudaError_t launch_q4_join(const AttendQ4Params& p, int grid, int split, cudaStream_t st) {
+inline cudaLaunchConfig_t q4_dependent(int grid, int threads, int smem, cudaStream_t st, cudaLaunchAttribute* attr) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, split);
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr->val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attend_q4_join_kernel<D>, p);
+  return cfg;
 }
 
-cudaError_t launch_attend_q4_tc(AttendQ4Params p, int d, cudaStream_t st);
+// The tensor-core kernel alone, as a programmatic dependent of the few-rows kernel that was launched before it: it reads
+// nothing of that one's, but ends after it.  `grid` and `part_rows` for the join are returned.
+cudaError_t launch_attend_q4_tc(AttendQ4Params p, int d, int* grid, int* part_rows, cudaStream_t st);
 
 }  // namespace pbsa

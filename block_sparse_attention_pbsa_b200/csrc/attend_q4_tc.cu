@@ -666,6 +666,8 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
   }
 
   // ----------------------------------------------------------------- teardown
+  // the kernel before may be running still: the join, which follows this one alone, needs both complete
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -675,7 +677,7 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
 }
 
 template <int D>
-cudaError_t launch_t(AttendQ4Params p, cudaStream_t st) {
+cudaError_t launch_t(AttendQ4Params p, int* grid, int* part_rows, cudaStream_t st) {
   auto kern = attend_q4_tc_kernel<D>;
   cudaError_t e = set_smem_once((const void*)kern, (int)TqSmem<D>::BYTES);
   if (e != cudaSuccess) return e;
@@ -683,21 +685,21 @@ cudaError_t launch_t(AttendQ4Params p, cudaStream_t st) {
   cudaFuncAttributes attr;
   if ((e = cudaFuncGetAttributes(&attr, kern)) != cudaSuccess) return e;
   if (attr.numRegs * 5 < (int)(REG_CTRL + 2 * REG_UNPACK + 2 * REG_SOFT)) return cudaErrorNotSupported;
-  p.part_rows = TQ_ROWS;
+  p.part_rows = *part_rows = TQ_ROWS;
   p.tile_cost = TQ_TILE_COST;
   int sms = 0, dev = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-  const int grid = sms < Q4_TC_MAX_CTAS ? sms : Q4_TC_MAX_CTAS;
-  kern<<<grid, TQ_THREADS, TqSmem<D>::BYTES, st>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_q4_join<D>(p, grid, 8, st);
+  *grid = sms < Q4_TC_MAX_CTAS ? sms : Q4_TC_MAX_CTAS;
+  cudaLaunchAttribute late;
+  const cudaLaunchConfig_t cfg = q4_dependent(*grid, TQ_THREADS, (int)TqSmem<D>::BYTES, st, &late);
+  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 }  // namespace
 
-cudaError_t launch_attend_q4_tc(AttendQ4Params p, int d, cudaStream_t st) {
-  return d == 128 ? launch_t<128>(p, st) : launch_t<64>(p, st);
+cudaError_t launch_attend_q4_tc(AttendQ4Params p, int d, int* grid, int* part_rows, cudaStream_t st) {
+  return d == 128 ? launch_t<128>(p, grid, part_rows, st) : launch_t<64>(p, grid, part_rows, st);
 }
 
 }  // namespace pbsa
