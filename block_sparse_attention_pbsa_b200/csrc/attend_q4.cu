@@ -40,7 +40,6 @@ constexpr int AQ_WARPS = 4;                       // computing warps
 constexpr int AQ_THREADS = (AQ_WARPS + 1) * 32;   // + the producer
 constexpr int AQ_STAGES = 3;                      // of two slots each
 constexpr int AQ_MIN_STEPS = 4;                   // blocks that are worth a CTA of their own
-constexpr int AQ_TILE_COST = 3;                   // blocks that a tile's start and end take the time of
 
 template <int D, int NT>
 struct AqSmem {
@@ -100,8 +99,8 @@ __global__ void __launch_bounds__(AQ_THREADS, NT == 1 && SPLIT == 1 ? 3 : 2) att
     fence_barrier_init();
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const Q4Share share = q4_share<AQ_THREADS>(p, ROWS, AQ_MIN_STEPS, &start_s);   // has block barriers
-  Q4Walk walk(p, share, start_s, ROWS);
+  const Q4Share share = q4_share<AQ_THREADS, false>(p, ROWS, Q4_FEW_COST, AQ_MIN_STEPS, &start_s);   // has block barriers
+  Q4Walk walk(p, share, start_s, ROWS, Q4_FEW_COST);
 
   if (warp == AQ_WARPS) {
     // ------------------------------------------------------------- producer
@@ -421,18 +420,18 @@ __global__ void __launch_bounds__(AQ_THREADS, NT == 1 && SPLIT == 1 ? 3 : 2) att
 }
 
 template <int D, int NT, int SPLIT>
-cudaError_t launch_t(AttendQ4Params* p, int* grid, cudaStream_t st) {
+cudaError_t launch_t(AttendQ4Params* p, bool many, int* grid, cudaStream_t st) {
   auto kern = attend_q4_kernel<D, NT, SPLIT>;
   constexpr int smem = AqSmem<D, NT>::TOTAL;
   cudaError_t e = set_smem_once((const void*)kern, smem);
   if (e != cudaSuccess) return e;
   p->part_rows = AqSmem<D, NT>::ROWS;
-  p->tile_cost = AQ_TILE_COST;
   const int per_sm = NT == 1 && SPLIT == 1 ? 3 : 2;
   int sms = 0, dev = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   *grid = sms * per_sm < Q4_MAX_CTAS ? sms * per_sm : Q4_MAX_CTAS;
+  p->few_ctas = many ? *grid : 0;
   kern<<<*grid, AQ_THREADS, smem, st>>>(*p);
   return cudaGetLastError();
 }
@@ -440,19 +439,15 @@ cudaError_t launch_t(AttendQ4Params* p, int* grid, cudaStream_t st) {
 template <int D>
 cudaError_t launch_d(AttendQ4Params p, int dtype, int max_rows, cudaStream_t st) {
   Q4JoinParams j = {};
-  // Requests of more than Q4_TC_ROWS rows fill enough of a 256-row tensor-core tile (attend_q4_tc.cu).
-  const bool many = dtype == PBSA_BF16 && max_rows > Q4_TC_ROWS;
-  p.rows_above = 0;
-  p.rows_to = many ? Q4_TC_ROWS : max_rows;
-  cudaError_t e = dtype == PBSA_F32 ? launch_t<D, 1, 3>(&p, &j.few, st)
-                  : max_rows <= 8   ? launch_t<D, 1, 1>(&p, &j.few, st)
-                                    : launch_t<D, 2, 1>(&p, &j.few, st);
+  const bool many = dtype == PBSA_BF16 && max_rows > Q4_TC_ROWS;   // some may go to the tensor-core kernel
+  p.max_rows = max_rows;
+  cudaError_t e = dtype == PBSA_F32 ? launch_t<D, 1, 3>(&p, false, &j.few, st)
+                  : max_rows <= 8   ? launch_t<D, 1, 1>(&p, false, &j.few, st)
+                                    : launch_t<D, 2, 1>(&p, many, &j.few, st);
   if (e != cudaSuccess) return e;
   j.p = p;
   if (many) {
     // its pieces lie behind the others: the two kernels may run at the same time
-    p.rows_above = Q4_TC_ROWS;
-    p.rows_to = max_rows;
     j.tc_desc = p.desc += Q4_MAX_CTAS;
     j.tc_ml = p.part_ml += Q4_FEW_ROWS;
     j.tc_o = p.part_o += (size_t)Q4_FEW_ROWS * D;

@@ -11,7 +11,9 @@ namespace pbsa {
 constexpr int Q4_MAX_CTAS = 480;      // of a grid of the few-rows kernel (16 rows a piece)
 constexpr int Q4_TC_MAX_CTAS = 160;   // of a grid of the tensor-core kernel (256 rows a piece)
 constexpr int Q4_FEW_ROWS = 2 * Q4_MAX_CTAS * 16, Q4_PART_ROWS = Q4_FEW_ROWS + 2 * Q4_TC_MAX_CTAS * 256;   // of all pieces
-constexpr int Q4_TC_ROWS = 80;        // requests with more rows go to the tensor-core kernel
+constexpr int Q4_TC_ROWS = 80;        // requests with more rows go to the tensor-core kernel,
+constexpr int Q4_TC_STEPS = 32;       // if they are more than this many blocks for each CTA of the few-rows kernel,
+constexpr int Q4_FEW_TILE = 16, Q4_FEW_COST = 3;   // which would take them in tiles of 16 rows
 
 // A tile that starts in this CTA and ends in a later one (pieces = 0: none).
 struct __align__(8) Q4Desc {
@@ -34,9 +36,9 @@ struct AttendQ4Params {
   long long o_ld;
   float* lse;
   int f32;
-  int rows_above, rows_to;   // this kernel's requests have rows_above < q_len * group <= rows_to
+  int max_rows;              // no request has more
+  int few_ctas;              // of the few-rows kernel, where the tensor-core kernel runs beside it (else 0)
   int part_rows;             // rows of a piece in the workspace
-  int tile_cost;             // blocks that a tile is charged beside its own
   Q4Desc* desc;
   float2* part_ml;           // (reference maximum in log2 units, sum) of a piece's row
   float* part_o;
@@ -92,7 +94,9 @@ struct Q4Request {
 };
 
 // A request whose numbers are out of range is left out (and recorded once, by the CTA that asks).
-__device__ __forceinline__ Q4Request q4_request(const AttendQ4Params& p, int r, int tile_rows, bool record) {
+// Requests of at most `above` or more than `to` rows have no tiles here.
+__device__ __forceinline__ Q4Request q4_request(const AttendQ4Params& p, int r, int tile_rows, int tile_cost, int above, int to,
+                                                bool record) {
   Q4Request x;
   x.q0 = p.q_start[r];
   x.q_len = p.q_len[r];
@@ -108,10 +112,10 @@ __device__ __forceinline__ Q4Request q4_request(const AttendQ4Params& p, int r, 
     return x;
   }
   const int rows = x.q_len * p.group;
-  if (rows <= p.rows_above || rows > p.rows_to) return x;   // the other kernel's
+  if (rows <= above || rows > to) return x;
   x.tiles = (rows + tile_rows - 1) / tile_rows;
-  x.blocks = p.tile_cost + max(1, (x.kv_len + BT - 1) / BT);   // a request without keys has its rows written too
-  if (p.causal && x.tiles > 1) x.base = p.tile_cost + (max(x.kv_len - x.q_len, 0) + BT - 1) / BT;
+  x.blocks = tile_cost + max(1, (x.kv_len + BT - 1) / BT);   // a request without keys has its rows written too
+  if (p.causal && x.tiles > 1) x.base = tile_cost + (max(x.kv_len - x.q_len, 0) + BT - 1) / BT;
   return x;
 }
 
@@ -123,19 +127,44 @@ struct Q4Start {
 struct Q4Share {
   long long total, x0, x1;
   int ctas;
+  int above, to;     // the rows of this kernel's requests
 };
 
 // This CTA's share [x0, x1) of the line, and its start in shared memory.  Every thread calls it.
-template <int THREADS>
-__device__ __forceinline__ Q4Share q4_share(const AttendQ4Params& p, int tile_rows, int min_steps, Q4Start* start) {
+// The tensor-core kernel has 2.7 times the rate, but its tiles of 256 rows want many keys each before they fill the GPU, and
+// a tile's start and end last 10 us: it takes the requests of more than Q4_TC_ROWS rows where they are enough work.  One
+// prompt, few-rows kernel against tensor-core kernel: 300 tokens of 12 heads 20 and 39 us, 512 tokens 27 and 47, 1000
+// tokens 51 and 52 (28 blocks for each CTA), 512 over 1536 49 and 49 (40), 1000 of 32 heads over 4000 393 and 192 (507).
+// At 16 requests over 3000: 48 rows 39 and 68 us, 72 rows 57 and 71; at 64 over 6000: 48 rows 207 and 346, 96 rows 395 and 355.
+template <int THREADS, bool TC>
+__device__ __forceinline__ Q4Share q4_share(const AttendQ4Params& p, int tile_rows, int tile_cost, int min_steps, Q4Start* start) {
   __shared__ long long sums[THREADS / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.R + THREADS - 1) / THREADS;
   const int r0 = min(tid * per, p.R), r1 = min(r0 + per, p.R);
+  Q4Share s;
+  s.above = TC ? Q4_TC_ROWS : 0;
+  s.to = p.max_rows;
+  if (p.few_ctas > 0) {
+    long long heavy = 0;
+    for (int r = r0; r < r1; ++r)
+      heavy += p.kv_heads * q4_request(p, r, Q4_FEW_TILE, Q4_FEW_COST, Q4_TC_ROWS, p.max_rows, false).head_steps();
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) heavy += __shfl_xor_sync(0xffffffffu, heavy, o);
+    if (lane == 0) sums[warp] = heavy;
+    __syncthreads();
+    heavy = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) heavy += sums[w];
+    __syncthreads();
+    const bool tc = heavy > (long long)Q4_TC_STEPS * p.few_ctas;   // (both kernels find the same)
+    if (TC && !tc) s.to = 0;
+    if (!TC && tc) s.to = Q4_TC_ROWS;
+  }
   long long mine = 0;
   Q4Request req;
   for (int r = r0; r < r1; ++r) {
-    req = q4_request(p, r, tile_rows, blockIdx.x == 0);
+    req = q4_request(p, r, tile_rows, tile_cost, s.above, s.to, blockIdx.x == 0);
     mine += p.kv_heads * req.head_steps();
   }
   long long upto = mine;
@@ -146,7 +175,6 @@ __device__ __forceinline__ Q4Share q4_share(const AttendQ4Params& p, int tile_ro
   }
   if (lane == 31) sums[warp] = upto;
   __syncthreads();
-  Q4Share s;
   s.total = 0;
   long long before = 0;
 #pragma unroll
@@ -167,7 +195,7 @@ __device__ __forceinline__ Q4Share q4_share(const AttendQ4Params& p, int tile_ro
     if (s.x0 >= at && s.x0 < at + mine) {   // one thread
       int r = r0;
       for (;; ++r) {
-        if (per > 1) req = q4_request(p, r, tile_rows, false);
+        if (per > 1) req = q4_request(p, r, tile_rows, tile_cost, s.above, s.to, false);
         const long long n = p.kv_heads * req.head_steps();
         if (s.x0 < at + n) break;
         at += n;
@@ -195,7 +223,7 @@ __device__ __forceinline__ Q4Share q4_share(const AttendQ4Params& p, int tile_ro
 struct Q4Walk {
   const AttendQ4Params& p;
   long long x, x1, total;
-  int ctas, tile_rows;
+  int ctas, tile_rows, tile_cost, above, to;
   Q4Request req;
   int r;
   int at;         // blocks of the current tile that lie before the next piece
@@ -204,8 +232,8 @@ struct Q4Walk {
   int piece;      // its place in the workspace; -1: the whole tile
   Q4Desc desc;    // the tile that goes on in a later CTA
 
-  __device__ Q4Walk(const AttendQ4Params& prm, const Q4Share& s, const Q4Start& start, int tr)
-      : p(prm), x(s.x0), x1(s.x1), total(s.total), ctas(s.ctas), tile_rows(tr) {
+  __device__ Q4Walk(const AttendQ4Params& prm, const Q4Share& s, const Q4Start& start, int tr, int cost)
+      : p(prm), x(s.x0), x1(s.x1), total(s.total), ctas(s.ctas), tile_rows(tr), tile_cost(cost), above(s.above), to(s.to) {
     desc.pieces = 0;
     if (x >= x1) return;
     req = start.req;
@@ -224,7 +252,7 @@ struct Q4Walk {
         mt = 0;
         if (++h == p.kv_heads) {
           h = 0;
-          do req = q4_request(p, ++r, tile_rows, false);
+          do req = q4_request(p, ++r, tile_rows, tile_cost, above, to, false);
           while (req.tiles == 0);   // there is one: x < x1
         }
       }

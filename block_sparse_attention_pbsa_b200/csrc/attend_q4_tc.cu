@@ -165,12 +165,18 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
   if (tid < 512) reinterpret_cast<uint32_t*>(sm + SM::ZERO)[tid] = 0u;
   fence_proxy_async_smem();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const Q4Share share = q4_share<TQ_THREADS, true>(p, TQ_ROWS, TQ_TILE_COST, TQ_MIN_STEPS, &start_s);   // has block barriers
+  if (share.x0 >= share.x1) {   // (often all CTAs: see there)
+    if (tid == 0) p.desc[blockIdx.x].pieces = 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   if (warp == 1) {
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
   }
   tc_fence_before();
-  const Q4Share share = q4_share<TQ_THREADS>(p, TQ_ROWS, TQ_MIN_STEPS, &start_s);   // has block barriers
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   auto wait = [&](int bar, uint32_t parity) {
@@ -195,7 +201,7 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
     if (warp == 2) {
       // ------------------------------------------------------------- walks the share
       if (lane == 0) {
-        Q4Walk walk(p, share, start_s, TQ_ROWS);
+        Q4Walk walk(p, share, start_s, TQ_ROWS, TQ_TILE_COST);
         bool more = true;
         for (int k = 0; more; ++k) {
           more = walk.next();
@@ -686,7 +692,6 @@ cudaError_t launch_t(AttendQ4Params p, int* grid, int* part_rows, cudaStream_t s
   if ((e = cudaFuncGetAttributes(&attr, kern)) != cudaSuccess) return e;
   if (attr.numRegs * 5 < (int)(REG_CTRL + 2 * REG_UNPACK + 2 * REG_SOFT)) return cudaErrorNotSupported;
   p.part_rows = *part_rows = TQ_ROWS;
-  p.tile_cost = TQ_TILE_COST;
   int sms = 0, dev = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;

@@ -21,9 +21,16 @@ def t_dtype(dtype):
 
 class Filled:
     """Requests of ``lens`` = [(step tokens, cached tokens before them)] whose whole K and V are in a 4-bit pool,
-    in shuffled slots; queries of the step.  ``rows_after``: rows of no request behind the last one."""
+    in shuffled slots; queries of the step.  ``rows_after``: rows of no request behind the last one.  ``heavy``: one more
+    request, enough work for the batch's requests of more than 80 rows (bf16) to go to the tensor-core kernel."""
 
-    def __init__(self, lens, q_heads, kv_heads, d, dtype, seed=0, rows_after=0, edit=None, slack=3, q_scale=1.0):
+    def __init__(self, lens, q_heads, kv_heads, d, dtype, seed=0, rows_after=0, edit=None, slack=3, q_scale=1.0, heavy=False):
+        if heavy:
+            # 16-row tiles of 125 blocks of 8000 tokens (and 3 for their own start and end), times heads: above 32 for
+            # each of the 2 * 148 CTAs of the few-rows kernel
+            tiles = -(-33 * 296 // (128 * kv_heads))
+            lens = list(lens) + [(max(16 * tiles * kv_heads // q_heads, 81), 8000)]
+        self.heavy = heavy
         self.lens, self.hq, self.hk, self.d, self.dtype = lens, q_heads, kv_heads, d, dtype
         dt = t_dtype(dtype)
         gen = torch.Generator().manual_seed(seed)
@@ -82,7 +89,13 @@ class Filled:
             L = n + p
             kk, vv = RO.held(k[kv:kv + L], v[kv:kv + L])
             o, lse, w = RO.attend(q[at:at + n], kk, vv, scale, causal)
-            out.append((o, lse) + self._bounds(q[at:at + n], k[kv:kv + L], v[kv:kv + L], o, lse, w, scale))
+            ob, lb = self._bounds(q[at:at + n], k[kv:kv + L], v[kv:kv + L], o, lse, w, scale)
+            if self.heavy and n * self.hq // self.hk > 80:
+                # the tensor-core form: p is rounded to bf16 (instead of p s), and so is each value: half a step of |v| each
+                g = self.hq // self.hk
+                for h in range(self.hq):
+                    ob[:, h] += 2.0 * U[self.q.dtype] * (w[h] @ np.abs(np.nan_to_num(vv[:, h // g])))
+            out.append((o, lse, ob, lb))
             at += n
             kv += L
         return out

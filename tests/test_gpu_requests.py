@@ -254,11 +254,41 @@ def test_long_prompts(lens, hq, hk, d, causal):
     f.check(*f.attend(causal), causal)
 
 
-def test_tiles_without_keys_among_others():
+@pytest.mark.parametrize("hq,hk,d", [(2, 2, 128), (4, 1, 128), (3, 1, 64), (10, 2, 64)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompts_and_decodes_beside_a_heavy_request(hq, hk, d, causal):
+    f = Filled(MANY, hq, hk, d, "bf16", seed=4, rows_after=3, heavy=True)
+    f.check(*f.attend(causal), causal)
+
+
+@pytest.mark.parametrize("lens,hq,hk,d,causal", [
+    ([(700, 0)], 4, 2, 128, True),
+    ([(300, 1500), (1, 90), (90, 0), (257, 31)], 6, 2, 128, True),
+    ([(130, 2000), (129, 63)], 8, 8, 64, False),
+    ([(513, 700), (0, 3), (2, 4000)], 3, 1, 64, True),
+    ([(5, 333), (4, 100), (1, 700)], 96, 1, 128, True),   # 96 heads share one: a single token fills a half
+    ([(25, 900), (130, 300), (64, 5), (300, 0)], 4, 2, 128, True),   # tiles with and without a second half
+    ([(60, 64), (120, 10), (64, 900), (70, 1), (90, 2)], 2, 1, 64, False),
+])
+def test_long_prompts_beside_a_heavy_request(lens, hq, hk, d, causal):
+    f = Filled(lens, hq, hk, d, "bf16", seed=14, rows_after=2, heavy=True)
+    f.check(*f.attend(causal), causal)
+
+
+@pytest.mark.parametrize("past", [3000, 4000, 4500, 5000, 6000])
+def test_either_side_of_the_choice_of_kernel(past):
+    """From a little less work than the tensor-core kernel is chosen for to a little more: the same sums, to rounding."""
+    f = Filled([(256, past), (1, 70), (90, 10)], 8, 4, 128, "bf16", seed=18)
+    f.heavy = True                                     # (the looser of the two bounds)
+    f.check(*f.attend(True), True)
+
+
+@pytest.mark.parametrize("heavy", [False, True])
+def test_tiles_without_keys_among_others(heavy):
     """Prompts of which only a few tokens are cached: whole row tiles see nothing, in the middle of a CTA's share
     and at its ends."""
     lens = [(200, 0), (140, 60), (300, 0), (200, 100)]
-    f = Filled(lens, 4, 1, 128, "bf16", seed=15)
+    f = Filled(lens, 4, 1, 128, "bf16", seed=15, heavy=heavy)
     full = f.kv_len.clone()
     f.kv_len[0] = 3
     f.kv_len[2] = 0
@@ -303,10 +333,11 @@ def test_rows_without_keys():
 
 @pytest.mark.parametrize("lens", [[(1, 700), (4, 300)], [(40, 900), (130, 300)]])
 @pytest.mark.parametrize("factor", [30.0, 1e4, 1e9, 1e20, 1e34])
-def test_large_scores(lens, factor):
+@pytest.mark.parametrize("heavy", [False, True])
+def test_large_scores(lens, factor, heavy):
     """Scores from hundreds to the end of fp32's range: the softmax picks one key, whose value is the output (where
     two keys' scores are nearer than fp32 can tell, any mix of theirs), and nothing overflows."""
-    f = Filled(lens, 4, 2, 128, "bf16", seed=16, q_scale=factor)
+    f = Filled(lens, 4, 2, 128, "bf16", seed=16, q_scale=factor, heavy=heavy)
     o, lse = f.attend(True)
     assert P.pbsa_get_device_error(f.ws) == 0
     assert torch.isfinite(o).all() and torch.isfinite(lse).all()
@@ -333,8 +364,8 @@ def test_large_scores(lens, factor):
         kv += n + p
 
 
-@pytest.mark.parametrize("lens", [[(1, 70), (1, 100)], [(40, 50), (130, 5)]])
-def test_values_that_are_not_finite_reach_only_the_rows_that_see_them(lens):
+@pytest.mark.parametrize("lens,heavy", [([(1, 70), (1, 100)], False), ([(40, 50), (130, 5)], False), ([(90, 50), (130, 5)], True)])
+def test_values_that_are_not_finite_reach_only_the_rows_that_see_them(lens, heavy):
     """A token that is not finite makes the rows that attend it NaN, and no others: not those it is masked for
     (later step tokens), not other requests."""
     def edit(f):
@@ -342,7 +373,7 @@ def test_values_that_are_not_finite_reach_only_the_rows_that_see_them(lens):
         f.k[p + n - 1, 0, 3] = float("nan")      # request 0's last token, head 0
         f.v[n + p, 1, 0] = float("inf")          # request 1's first token, head 1
 
-    f = Filled(lens, 4, 2, 128, "bf16", seed=8, edit=edit)
+    f = Filled(lens, 4, 2, 128, "bf16", seed=8, edit=edit, heavy=heavy)
     o, lse = f.attend(True)
     f.check(o, lse, True)
     n = lens[0][0]
@@ -361,6 +392,24 @@ def test_bad_requests_are_left_out():
     assert torch.equal(o[6:], want[6:])
 
 
+def test_bad_slots_and_requests_beside_a_heavy_request():
+    """The tensor-core kernel: a slot outside the pool is recorded and its tokens left out, a bad request is left out."""
+    f = Filled([(100, 150), (120, 40)], 2, 2, 64, "bf16", seed=19, heavy=True)
+    want, _ = f.attend(True)
+    f.table[0, 1] = f.slots + 3
+    f.kv_len[1] = 64 * f.ld + 1
+    o, lse = f.attend(True)
+    assert P.pbsa_get_device_error(f.ws) == 5
+    assert (o[100:220] == 7).all() and (lse[:, 100:220] == 7).all()
+    assert torch.equal(o[220:], want[220:]) or (o[220:] - want[220:]).abs().max() <= 2.0 ** -6   # (shares lie otherwise)
+    keep = np.r_[0:64, 128:250]
+    k, v = f.k[:250].double().numpy(), f.v[:250].double().numpy()
+    kk, vv = RO.held(k[keep], v[keep])
+    wo, wl, _ = RO.attend(f.q[:100].double().numpy(), kk, vv, float(np.float32(64 ** -0.5)), True)
+    assert np.abs(o[:100].double().cpu().numpy() - wo).max() <= 2.0 ** -6 * np.abs(vv).max()
+    assert np.abs(lse[:, :100].double().cpu().numpy() - wl).max() <= 1e-4
+
+
 def test_bad_slot_is_left_out_of_the_sums():
     f = Filled([(1, 150)], 2, 2, 128, "bf16", seed=10)
     f.table[0, 1] = f.slots + 3
@@ -373,10 +422,10 @@ def test_bad_slot_is_left_out_of_the_sums():
     assert np.abs(lse.double().cpu().numpy() - wl).max() <= 1e-4
 
 
-@pytest.mark.parametrize("lens,causal", [(FEW, True), (MANY, False)])
-def test_strided_queries_and_outputs(lens, causal):
+@pytest.mark.parametrize("lens,causal,heavy", [(FEW, True, False), (MANY, False, False), (MANY, True, True)])
+def test_strided_queries_and_outputs(lens, causal, heavy):
     """q as a slice of a projection's output, o inside a wider buffer."""
-    f = Filled(lens, 4, 2, 128, "bf16", seed=11)
+    f = Filled(lens, 4, 2, 128, "bf16", seed=11, heavy=heavy)
     T = f.tokens
     wide = torch.zeros((T, 8, 128), dtype=torch.bfloat16, device=DEV)
     wide[:, :4] = f.q.to(DEV)
@@ -386,9 +435,9 @@ def test_strided_queries_and_outputs(lens, causal):
     assert (out[:, 0] == 7).all() and (out[:, 5] == 7).all()
 
 
-@pytest.mark.parametrize("lens", [FEW, MANY])
-def test_same_bits_every_time_and_without_lse(lens):
-    f = Filled(lens, 8, 2, 128, "bf16", seed=12)
+@pytest.mark.parametrize("lens,heavy", [(FEW, False), (MANY, False), (MANY, True)])
+def test_same_bits_every_time_and_without_lse(lens, heavy):
+    f = Filled(lens, 8, 2, 128, "bf16", seed=12, heavy=heavy)
     o, lse = f.attend(True)
     for _ in range(3):
         o2, lse2 = f.attend(True)
@@ -399,8 +448,9 @@ def test_same_bits_every_time_and_without_lse(lens):
     assert torch.equal(o, o3)
 
 
-def test_the_workspace_may_hold_anything_behind_its_error_word():
-    f = Filled(FEW + [(1, 3000)], 8, 2, 128, "bf16", seed=13)
+@pytest.mark.parametrize("heavy", [False, True])
+def test_the_workspace_may_hold_anything_behind_its_error_word(heavy):
+    f = Filled(FEW + [(1, 3000)], 8, 2, 128, "bf16", seed=13, heavy=heavy)
     o, lse = f.attend(True)
     f.ws[256:] = 0xFF
     o2, lse2 = f.attend(True)
