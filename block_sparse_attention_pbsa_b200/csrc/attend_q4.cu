@@ -13,13 +13,10 @@
 // are the 16 rows, query rows the 8 columns, and the codes go from shared memory through a shift
 // and a lop3 straight into A fragments.  (tcgen05 reads A from TMEM or shared memory: a code
 // would be written back once before it is used, and 128 rows would hold 8.)
-//  * Work: the blocks of every (request, row tile, kv head), in that order, are one line; CTA i of
-//    N takes the i-th N-th of it.  Each CTA sums the lengths for itself, so no host knowledge of the
-//    lengths is needed and a captured call follows them.  A tile that crosses CTAs is written as
-//    partial (o, maximum, sum) per piece, and a second kernel, launched as a programmatic dependent,
-//    joins the pieces in order.  At most one tile starts in a CTA and ends in a later one, so a CTA
-//    has two slots for pieces.  Nothing carries over from call to call.
-//  * A producer warp brings whole slots (8704 bytes: K, V, scales) with one bulk copy each into a ring of pairs;
+//  * Work: the line of attend_q4.cuh.  A tile that crosses CTAs is written as partial (o, maximum, sum) per piece, and
+//    a second kernel, launched as a programmatic dependent, joins the pieces in order.  At most one tile starts
+//    in a CTA and ends in a later one, so a CTA has two places for pieces.  Nothing carries over from call to call.
+//  * A producer warp brings whole slots (8704 bytes: K, V, scales) with one bulk copy each into a ring of three pairs;
 //    four warps take 16 tokens of each slot, with a running maximum and sum of their own, joined
 //    in shared memory at a tile's end.  The reference maximum moves only when a score exceeds it by
 //    2^8, which one vote per 16 tokens detects.
@@ -29,6 +26,13 @@
 //    products are fp32 products.
 // A slot id outside the pool is recorded and its block skipped.  Waits are bounded; on expiry the
 // error is recorded, copies in flight are waited for, and the kernel winds down.
+//
+// Measured (D = 128, bf16; 6.5 TB/s is a plain copy's rate): 32 tokens of 32 heads (8 kv heads) over 16000 .. 60000
+// cached ones, 1.37 GB: 287-300 us, 4.6-4.8 TB/s; the loads alone take 229 us.  48 tokens over 300 .. 8192, 229 MB:
+// 60 us, 3.8 TB/s.  One token of 12 heads over 1536: 8.8 us, of which the join and the launches are 3.
+// What bounds it: 290 warp instructions for 16 tokens of a head, 112 of them shifts and masks (128 codes a lane); the
+// issue slots are 56% busy, the integer pipe 60%, HBM 65-70%.  Three CTAs an SM at 128 registers: two (with four
+// pairs in the ring) take 303 us, four at 96 registers 324 us.  Two slots side by side: 290 us, one after the other 308.
 #include <math.h>
 
 #include "attend_q4.cuh"
@@ -39,7 +43,9 @@ namespace {
 constexpr int AQ_WARPS = 4;                       // computing warps
 constexpr int AQ_THREADS = (AQ_WARPS + 1) * 32;   // + the producer
 constexpr int AQ_STAGES = 3;                      // of two slots each
-constexpr int AQ_MIN_STEPS = 4;                   // blocks that are worth a CTA of their own
+// Blocks (a tile's own cost included) that are worth a CTA: with 2, 4 and 8 one token of 12 heads over 1536 takes 9.7,
+// 9.2 and 11.0 us, over 8000 14.8, 14.9 and 13.9 us.
+constexpr int AQ_MIN_STEPS = 4;
 
 template <int D, int NT>
 struct AqSmem {
@@ -439,7 +445,8 @@ cudaError_t launch_t(AttendQ4Params* p, bool many, int* grid, cudaStream_t st) {
 template <int D>
 cudaError_t launch_d(AttendQ4Params p, int dtype, int max_rows, cudaStream_t st) {
   Q4JoinParams j = {};
-  const bool many = dtype == PBSA_BF16 && max_rows > Q4_TC_ROWS;   // some may go to the tensor-core kernel
+  // some may go to the tensor-core kernel, which the lengths decide (q4_share)
+  const bool many = dtype == PBSA_BF16 && max_rows > Q4_TC_ROWS;
   p.max_rows = max_rows;
   cudaError_t e = dtype == PBSA_F32 ? launch_t<D, 1, 3>(&p, false, &j.few, st)
                   : max_rows <= 8   ? launch_t<D, 1, 1>(&p, false, &j.few, st)

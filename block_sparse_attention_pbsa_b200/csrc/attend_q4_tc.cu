@@ -6,7 +6,8 @@
 // tile: the products, the exponentials and the unpacking of the codes bound it.
 //  * Work: the line of attend_q4.cuh, with tiles of 256 rows in two halves, so that a key unpacked once serves
 //    both; one CTA per SM, pieces one after another (one warp walks them and tells the others).  With the causal rule
-//    a tile is charged what it sees, so long prompts are spread evenly.
+//    a tile is charged what it sees, so long prompts are spread evenly.  The kernel runs as a programmatic dependent
+//    beside the few-rows kernel's last CTAs, from which it reads nothing.
 //  * Each step covers two blocks (128 keys).  One thread each brings K's and V's bytes with bulk copies;
 //    two warpgroups, alternate steps, unpack them into shared-memory operand tiles (128-byte swizzle): K as
 //    the codes themselves (plus 128, exact in bf16), V as bf16 values s*c + m, rounded once, the bits that
@@ -30,6 +31,14 @@
 //    that are not cached is zero, so whatever bytes lie there reach no row.
 // Waits are bounded; on expiry the error is recorded and every role runs through its pieces without
 // waiting, drains its copies and MMAs, frees TMEM and returns.
+//
+// Measured (D = 128): 4608 tokens of 12 heads over 13824, without the causal rule: 665-680 us, 575-590 TFLOP/s (0.34
+// of the measured 1685); three prompts of 700 .. 2048 tokens of 32 heads (8 kv heads) over 1000 .. 14000: 985-1008 us, 540
+// TFLOP/s.  A step of 256 rows and 128 keys lasts about 6400 cycles; its MMAs take 2800 of the tensor pipe's, its
+// exponentials 2048 of either unit's.  What bounds it is the chain of a half: a pass over 128 scores a thread (about
+// 3700 cycles, the unpacking and the other half in the same issue slots), then P V and the next Q K^T before S is there
+// again.  TMEM holds S and O of two halves and no third.  Tiles of 128 rows took 707 and 1168 us, two threads a row
+// 819 and 1219 (registers), the maximum found before the exponentials 799 and 1205.
 #include <math.h>
 
 #include "attend_q4.cuh"
@@ -39,8 +48,12 @@ namespace {
 
 constexpr int TQ_THREADS = 640;      // warpgroups: control, unpack x 2, softmax x 2
 constexpr int TQ_ROWS = 256;         // two halves of 128
-constexpr int TQ_MIN_STEPS = 8;      // blocks that are worth a CTA of their own
-constexpr int TQ_TILE_COST = 12;     // blocks that a tile's start and end and its two passes over masked steps cost
+// Blocks that are worth a CTA: with 4, 8, 16 and 32 one prompt of 300 tokens over 3000 took 49, 58, 70 and 90 us, 64
+// tokens over 30000 86, 77, 74 and 94 us.
+constexpr int TQ_MIN_STEPS = 8;
+// Blocks that a tile's start and end and its second passes over masked steps cost: charged 0, 8, 12, 16 and 24, the three
+// prompts take 1063, 1003, 984, 984 and 1009 us, the chunk of 4608 tokens 672, 661, 664, 669 and 677.
+constexpr int TQ_TILE_COST = 12;
 constexpr int STAGES = 2, SCS = 4;   // operand stages of K and of V, key scales
 constexpr uint32_t REG_CTRL = 48, REG_UNPACK = 80, REG_SOFT = 136;   // launched with 96: 48 + 2*80 + 2*136 = 5*96
 static_assert(REG_CTRL + 2 * REG_UNPACK + 2 * REG_SOFT <= 5 * 96, "register split exceeds the launch");
@@ -532,7 +545,7 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
         bool careful = __any_sync(0xffffffffu, see < 128 || R == -INFINITY || fabsf(R) > 4096.f) || ok != 3;
         bool plain = true, passed = false;
         // The halves take turns, so that one's pass runs beside the other's products; the turn is passed on after five
-        // of eight chunks (at the end: 716 us for the chunk of 4608 tokens, here 683, without turns 701).
+        // of eight chunks (at the end: 716 us for the chunk of 4608 tokens, here 677, without turns 701).
         if (both && (half == 1 || turn > 0)) wait(T_TURN + (half ^ 1), (half == 1 ? turn : turn - 1) & 1);
 #pragma unroll 1
         while (true) {

@@ -16,7 +16,9 @@
 // without one.  Table rows and the free stack need no barrier: a call reads table entries below
 // blocks(len_r) and stack entries below the free count, and writes only entries at or above them.
 //
-// Bound by latency (the sums, a binary search per token, one dependent table read), not bytes.
+// Bound by latency (the sums, a binary search per token, one dependent table read), not bytes: 64 requests of a
+// token 4.7 us, 1024 requests with 49152 rows 8.2 us apart (16.4 us as the one cluster of 8 CTAs, which the state in
+// place needs); 0.45 MB, 0.07 us at a copy's rate.
 #include "common.cuh"
 #include "internal.h"
 
