@@ -58,6 +58,7 @@ def make_req_geom(q_heads, kv_heads, head_dim, scale, dtype) -> ReqGeom:
 
 
 _lib = None
+_binding = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _L = ctypes.c_longlong
@@ -103,7 +104,7 @@ OPTIONAL = {}
 
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load libpbsa.so (raises if it is absent: there is no fallback path)."""
-    global _lib
+    global _lib, _binding
     if _lib is not None:
         return _lib
     if not os.path.exists(path):
@@ -117,6 +118,15 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             continue
         f = getattr(lib, name)
         f.restype, f.argtypes = res, args
+    try:
+        from . import _requests as binding
+    except ImportError as e:
+        raise RuntimeError(f"the binding _requests.so cannot be imported ({e}); build it with "
+                           "`python -m block_sparse_attention_pbsa_b200.build`") from e
+    binding.bind(*(ctypes.cast(getattr(lib, name), _P).value for name in (
+        "pbsa_request_tables", "pbsa_append_q4", "pbsa_expand_q4", "pbsa_attend_q4", "pbsa_q4_block_bytes",
+        "pbsa_attend_q4_workspace_bytes")))
+    _binding = binding
     _lib = lib
     return lib
 
@@ -308,58 +318,6 @@ def pbsa_attend_bwd(g: Geom, q, q_frames, k_pool, v_pool, pool_slots, kv_slot, k
 PBSA_CAUSAL = 1
 
 
-# These calls are made per layer and step, so the checks are kept to a few attribute reads a tensor.
-_I32 = torch.int32
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # the current stream's handle, without a Stream object
-_Q4_SIZES = {}                                                       # head_dim -> (bytes of a slot, of the workspace)
-
-
-def _call_env(stream):
-    """(current device, its stream's handle) of a call."""
-    dev = torch.cuda.current_device()
-    if stream is not None:
-        return dev, stream.cuda_stream
-    return dev, _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
-
-
-def _dev(t, dtype, name, numel, index):
-    """Device pointer (an int) of a contiguous tensor of device ``index`` (of ``numel`` elements, unless None)."""
-    if t.get_device() != index:
-        raise ValueError(f"{name} must be a tensor of the current CUDA device")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if numel is not None and t.numel() != numel:
-        raise ValueError(f"{name} must have {numel} elements, got {t.numel()}")
-    return t.data_ptr()
-
-
-def _tokens(t, dtype, name, heads, d, index):
-    """(pointer, elements between tokens, tokens) of [tokens, heads, d] whose tokens may lie apart."""
-    if t.get_device() != index:
-        raise ValueError(f"{name} must be a tensor of the current CUDA device")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    shape = t.shape
-    if len(shape) != 3 or shape[1] != heads or shape[2] != d:
-        raise ValueError(f"{name} must be [tokens, {heads}, {d}], got {list(shape)}")
-    n, (ld, sh, se) = shape[0], t.stride()
-    if n and (se != 1 or (heads > 1 and sh != d)):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), (ld if n > 1 else heads * d), n
-
-
-def _ws(ws, index, need=256):
-    if ws is None:
-        return None
-    if ws.get_device() != index:
-        raise ValueError("ws must be a tensor of the current CUDA device")
-    if not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
-        raise ValueError(f"ws must be contiguous and hold {need} bytes")
-    return ws.data_ptr()
-
-
 def pbsa_q4_block_bytes(g: ReqGeom) -> int:
     return int(load().pbsa_q4_block_bytes(ctypes.byref(g)))
 
@@ -368,65 +326,34 @@ def pbsa_attend_q4_workspace_bytes(g: ReqGeom) -> int:
     return int(load().pbsa_attend_q4_workspace_bytes(ctypes.byref(g)))
 
 
-def _q4_sizes(g):
-    """Both sizes, which depend on head_dim alone, asked once (0 for a geometry that the call then refuses)."""
-    hit = _Q4_SIZES.get(g.head_dim)
-    if hit is None:
-        hit = (pbsa_q4_block_bytes(g), pbsa_attend_q4_workspace_bytes(g))
-        if hit[0]:
-            _Q4_SIZES[g.head_dim] = hit
-    return hit
+# These calls are made per layer and step: their arguments are checked in requests_binding.cpp, which raises ValueError
+# for tensors of another device, type, shape or layout than the call takes.
 
-
-def _rows(t, name):
-    shape = t.shape
-    if len(shape) != 2:
-        raise ValueError(f"{name} must be two-dimensional")
-    return shape
+def _requests():
+    load()
+    return _binding
 
 
 def pbsa_request_tables(step_len, seq_len, block_table, free_slot, free_cnt, q_start, q_len, kv_len, free_cnt_out,
                         slot_map, position=None, ws=None, stream=None):
     """Sizes are the tensors': requests of ``step_len``, table_ld of ``block_table`` [requests, table_ld], slots
     of ``free_slot``, tokens of ``slot_map``."""
-    dev, st = _call_env(stream)
-    R, ld = _rows(block_table, "block_table")
-    T, S = slot_map.numel(), free_slot.numel()
-    code = load().pbsa_request_tables(
-        _dev(step_len, _I32, "step_len", R, dev), _dev(seq_len, _I32, "seq_len", R, dev), R,
-        _dev(block_table, _I32, "block_table", None, dev), ld, _dev(free_slot, _I32, "free_slot", None, dev),
-        _dev(free_cnt, _I32, "free_cnt", 1, dev), S, T, _dev(q_start, _I32, "q_start", R + 1, dev),
-        _dev(q_len, _I32, "q_len", R, dev), _dev(kv_len, _I32, "kv_len", R, dev),
-        _dev(free_cnt_out, _I32, "free_cnt_out", 1, dev), _dev(slot_map, _I32, "slot_map", None, dev) if T else None,
-        None if position is None else _dev(position, _I32, "position", T, dev), _ws(ws, dev), st)
+    code = _requests().request_tables(step_len, seq_len, block_table, free_slot, free_cnt, q_start, q_len, kv_len,
+                                      free_cnt_out, slot_map, position, ws, stream)
     if code:
         raise PBSAError("pbsa_request_tables", code)
 
 
 def pbsa_append_q4(g: ReqGeom, k, v, slot_map, pool, pool_slots, ws=None, stream=None):
     """``k``, ``v`` [tokens, kv_heads, head_dim]; tokens may lie apart (a slice of a projection's output)."""
-    dev, st = _call_env(stream)
-    dt, H, d = _tok_dtype(g), g.kv_heads, g.head_dim
-    kp, kl, n = _tokens(k, dt, "k", H, d, dev)
-    vp, vl, m = _tokens(v, dt, "v", H, d, dev)
-    if m != n:
-        raise ValueError("k and v must have the same number of tokens")
-    code = load().pbsa_append_q4(
-        g, kp, kl, vp, vl, n, _dev(slot_map, _I32, "slot_map", n, dev),
-        _dev(pool, torch.uint8, "pool", H * pool_slots * _q4_sizes(g)[0], dev), pool_slots, _ws(ws, dev), st)
+    code = _requests().append_q4(g, k, v, slot_map, pool, pool_slots, ws, stream)
     if code:
         raise PBSAError("pbsa_append_q4", code)
 
 
 def pbsa_expand_q4(g: ReqGeom, pool, pool_slots, src_slot, k_pool, v_pool, ws=None, stream=None):
     """``k_pool``, ``v_pool`` [kv_heads, len(src_slot), 64, head_dim]."""
-    dev, st = _call_env(stream)
-    dt, H, d, n = _tok_dtype(g), g.kv_heads, g.head_dim, src_slot.numel()
-    size = H * n * 64 * d
-    code = load().pbsa_expand_q4(
-        g, _dev(pool, torch.uint8, "pool", H * pool_slots * _q4_sizes(g)[0], dev), pool_slots,
-        _dev(src_slot, _I32, "src_slot", None, dev), n, _dev(k_pool, dt, "k_pool", size, dev),
-        _dev(v_pool, dt, "v_pool", size, dev), _ws(ws, dev), st)
+    code = _requests().expand_q4(g, pool, pool_slots, src_slot, k_pool, v_pool, ws, stream)
     if code:
         raise PBSAError("pbsa_expand_q4", code)
 
@@ -435,24 +362,8 @@ def pbsa_attend_q4(g: ReqGeom, q, q_start, q_len, kv_len, max_q_len, pool, pool_
                    lse=None, ws=None, stream=None):
     """``q``, ``o`` [tokens, q_heads, head_dim]; tokens may lie apart.  ``q_start`` holds one entry per request or
     one more (as pbsa_request_tables writes it)."""
-    dev, st = _call_env(stream)
-    dt, Hq, d = _tok_dtype(g), g.q_heads, g.head_dim
-    qp, ql, n = _tokens(q, dt, "q", Hq, d, dev)
-    op, ol, m = _tokens(o, dt, "o", Hq, d, dev)
-    if m != n:
-        raise ValueError("o must have q's tokens")
-    R, ld = _rows(block_table, "block_table")
-    if q_start.numel() not in (R, R + 1):
-        raise ValueError(f"q_start must have {R} or {R + 1} elements, got {q_start.numel()}")
-    if ws is None:
-        raise ValueError("pbsa_attend_q4 needs a workspace")
-    block, need = _q4_sizes(g)
-    code = load().pbsa_attend_q4(
-        g, qp, ql, n, _dev(q_start, _I32, "q_start", None, dev), _dev(q_len, _I32, "q_len", R, dev),
-        _dev(kv_len, _I32, "kv_len", R, dev), R, max_q_len,
-        _dev(pool, torch.uint8, "pool", g.kv_heads * pool_slots * block, dev), pool_slots,
-        _dev(block_table, _I32, "block_table", None, dev), ld, PBSA_CAUSAL if causal else 0, op, ol,
-        None if lse is None else _dev(lse, torch.float32, "lse", Hq * n, dev), _ws(ws, dev, need), st)
+    code = _requests().attend_q4(g, q, q_start, q_len, kv_len, max_q_len, pool, pool_slots, block_table, causal, o, lse,
+                                 ws, stream)
     if code:
         raise PBSAError("pbsa_attend_q4", code)
 

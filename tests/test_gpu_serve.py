@@ -237,3 +237,59 @@ def test_batch_state_can_be_saved_and_resumed():
         assert torch.equal(getattr(a, name), getattr(b, name)), name
     with pytest.raises(ValueError):
         P.RequestBatch(P.RequestConfig(3, 4, 100, 9)).load_state_dict(st)
+
+
+def test_the_binding_refuses_what_the_calls_do_not_take():
+    """Types, shapes, layouts, devices and sizes that are refused before anything is launched."""
+    g = P.make_req_geom(4, 2, 64, 0.1, "bf16")
+    i = lambda n: torch.zeros(n, dtype=torch.int32, device=DEV)  # noqa: E731
+    x = lambda h, t=8, dt=torch.bfloat16: torch.zeros((t, h, 64), dtype=dt, device=DEV)  # noqa: E731
+    pool = torch.zeros(2 * 3 * 4608, dtype=torch.uint8, device=DEV)
+    ws = torch.zeros(P.pbsa_attend_q4_workspace_bytes(g), dtype=torch.uint8, device=DEV)
+
+    def tables(**kw):
+        a = dict(step_len=i(3), seq_len=i(3), block_table=i(6).view(3, 2), free_slot=i(5), free_cnt=i(1), q_start=i(4), q_len=i(3),
+                 kv_len=i(3), free_cnt_out=i(1), slot_map=i(9), position=i(9))
+        P.pbsa_request_tables(*{**a, **kw}.values(), ws=None)
+    tables()
+    for kw in (dict(step_len=i(4)), dict(seq_len=i(3).cpu()), dict(block_table=i(6)), dict(q_start=i(3)), dict(position=i(8)),
+               dict(free_cnt=i(2)), dict(slot_map=i(18)[::2]), dict(kv_len=i(3).long()), dict(q_len=None)):
+        with pytest.raises(ValueError):
+            tables(**kw)
+    with pytest.raises(P.PBSAError):
+        tables(free_slot=i(0))                                   # a pool without slots
+
+    def append(k=None, v=None, m=None, p=pool, slots=3, w=None):
+        P.pbsa_append_q4(g, x(2) if k is None else k, x(2) if v is None else v, i(8) - 1 if m is None else m, p, slots, ws=w)
+    append()
+    for kw in (dict(k=x(3)), dict(k=x(2, dt=torch.float32)), dict(k=x(2, 7)), dict(v=x(4)[:, ::2]), dict(m=i(7)), dict(slots=4),
+               dict(p=pool.view(torch.int8)), dict(w=ws[:100]), dict(k=x(2).cpu())):
+        with pytest.raises(ValueError):
+            append(**kw)
+    with pytest.raises(P.PBSAError):
+        append(k=torch.zeros((8, 2 * 64 + 4), dtype=torch.bfloat16, device=DEV)[:, :128].unflatten(1, (2, 64)))   # 8-byte rows
+    with pytest.raises(P.PBSAError):
+        append(k=x(2)[:1].expand(8, 2, 64))                      # every token the same memory
+    with pytest.raises(TypeError):
+        append(slots="3")
+
+    def attend(q=None, o=None, start=None, n=1, table=None, lse=None, w=ws, slots=3):
+        P.pbsa_attend_q4(g, x(4) if q is None else q, i(4) if start is None else start, i(3), i(3), n, pool, slots,
+                         i(6).view(3, 2) if table is None else table, True, x(4) if o is None else o, lse, ws=w)
+    attend()
+    attend(start=i(3))
+    for kw in (dict(q=x(2)), dict(o=x(4, 9)), dict(start=i(5)), dict(table=i(6)), dict(table=i(8).view(4, 2)), dict(w=None),
+               dict(w=ws[:-16]), dict(lse=torch.zeros(31, device=DEV)), dict(lse=x(4)), dict(slots=2), dict(n=1 << 40)):
+        with pytest.raises(ValueError):
+            attend(**kw)
+    with pytest.raises(P.PBSAError):
+        attend(w=torch.zeros(ws.numel() + 8, dtype=torch.uint8, device=DEV)[8:])        # 8-byte aligned
+
+    def expand(src=None, k=None, v=None):
+        d = torch.zeros((2, 2, 64, 64), dtype=torch.bfloat16, device=DEV)
+        P.pbsa_expand_q4(g, pool, 3, i(2) if src is None else src, d if k is None else k, d.clone() if v is None else v)
+    expand()
+    for kw in (dict(src=i(3)), dict(k=torch.zeros((2, 2, 64, 64), device=DEV)), dict(v=x(2)), dict(src=i(2).float())):
+        with pytest.raises(ValueError):
+            expand(**kw)
+    torch.cuda.synchronize()
