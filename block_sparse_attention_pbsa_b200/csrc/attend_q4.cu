@@ -414,8 +414,7 @@ __global__ void __launch_bounds__(AQ_THREADS, NT == 1 && SPLIT == 1 ? 3 : 2) att
         if (walk.piece < 0) {
           q4_write_row<D>(p, walk.q0, row0 + r, walk.h, 4 * ch, acc, M, L, ch == 0);
         } else {
-          *reinterpret_cast<float4*>(p.part_o + ((size_t)walk.piece * p.part_rows + r) * D + 4 * ch) =
-              make_float4(acc[0], acc[1], acc[2], acc[3]);
+          *q4_few_place<D>(p.part_o, p.part_rows, walk.piece, r, ch) = make_float4(acc[0], acc[1], acc[2], acc[3]);
           if (ch == 0) p.part_ml[(size_t)walk.piece * p.part_rows + r] = make_float2(M, L);
         }
       }

@@ -301,6 +301,10 @@ struct Q4Walk {
 // 2^(m - M) of a piece's sums; the sums of a piece that saw no key are zeros (or NaN, which stay)
 __device__ __forceinline__ float q4_weight(float m, float M) { return m == -INFINITY ? 1.f : ex2_approx(m - M); }
 
+__device__ __forceinline__ float q4_lse(float M, float L) {
+  return L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+}
+
 // Four channels of an output row, and its lse.
 template <int D>
 __device__ __forceinline__ void q4_write_row(const AttendQ4Params& p, int q0, int row, int h, int ch, const float (&acc)[4],
@@ -316,14 +320,32 @@ __device__ __forceinline__ void q4_write_row(const AttendQ4Params& p, int q0, in
         make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
   }
   if (with_lse && p.lse != nullptr)
-    p.lse[(size_t)head * p.T + q0 + tok] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+    p.lse[(size_t)head * p.T + q0 + tok] = q4_lse(M, L);
 }
 
-// Four channels of a row of the tile that starts in CTA `cta` and ends in a later one: its pieces joined, in order.
+__device__ __forceinline__ Q4Desc q4_desc(const Q4Desc* p) {
+  const int2* w = reinterpret_cast<const int2*>(p);
+  const int2 a = __ldcg(w), b = __ldcg(w + 1), c = __ldcg(w + 2);
+  return {a.x, a.y, b.x, b.y, c.x, c.y};
+}
+
+// Where channels 4 ch .. of row r of a piece lie in the workspace.  The few-rows kernel writes rows, a row's
+// channels by neighbouring threads; the tensor-core kernel has a thread for each row, so there the rows of four
+// channels are neighbours.
 template <int D>
+__device__ __forceinline__ float4* q4_few_place(float* part_o, int part_rows, int piece, int r, int ch) {
+  return reinterpret_cast<float4*>(part_o) + ((size_t)piece * part_rows + r) * (D / 4) + ch;
+}
+template <int D>
+__device__ __forceinline__ float4* q4_tc_place(float* part_o, int part_rows, int piece, int r, int ch) {
+  return reinterpret_cast<float4*>(part_o) + ((size_t)piece * (D / 4) + ch) * part_rows + r;
+}
+
+// Channels 4 ch .. of a row of the tile that starts in CTA `cta` and ends in a later one: its pieces joined, in order.
+template <int D, bool TC>
 __device__ __forceinline__ void q4_join_row(const AttendQ4Params& p, const Q4Desc& d, int cta, const float2* part_ml,
-                                            const float* part_o, int part_rows, int r, int ch) {
-  auto at = [&](int k) { return (size_t)(k == 0 ? 2 * cta + 1 : 2 * (cta + k)) * part_rows; };
+                                            float* part_o, int part_rows, int r, int ch) {
+  auto at = [&](int k) { return k == 0 ? 2 * cta + 1 : 2 * (cta + k); };
   // 8 pieces at a time, their loads in flight together (a place past the end repeats the last piece, unused)
   float M = -INFINITY, L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
@@ -332,9 +354,9 @@ __device__ __forceinline__ void q4_join_row(const AttendQ4Params& p, const Q4Des
     float4 v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const size_t place = at(min(k0 + i, d.pieces - 1)) + r;
-      ml[i] = part_ml[place];
-      v[i] = *reinterpret_cast<const float4*>(part_o + place * D + 4 * ch);
+      const int piece = at(min(k0 + i, d.pieces - 1));
+      ml[i] = __ldcg(part_ml + (size_t)piece * part_rows + r);   // (from L2: this grid may have started before they were written)
+      v[i] = __ldcg(TC ? q4_tc_place<D>(part_o, part_rows, piece, r, ch) : q4_few_place<D>(part_o, part_rows, piece, r, ch));
     }
     float top = M;
 #pragma unroll
@@ -367,7 +389,7 @@ struct Q4JoinParams {
   AttendQ4Params p;          // descriptors and pieces are the few-rows kernel's
   const Q4Desc* tc_desc;     // ... and these the tensor-core kernel's
   const float2* tc_ml;
-  const float* tc_o;
+  float* tc_o;
   int tc_rows, few, tc;      // CTAs of either
 };
 
@@ -375,18 +397,18 @@ template <int D>
 __global__ void __launch_bounds__(256) attend_q4_join_kernel(const Q4JoinParams jp) {
   __shared__ int counts[8], list[Q4_TC_MAX_CTAS];
   constexpr int CH = D / 4, RPP = 256 / CH, PARTS = 256 / RPP;
-  const int tid = threadIdx.x, ch = tid % CH;
+  const int tid = threadIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if ((int)blockIdx.x < jp.few) {
-    const Q4Desc d = jp.p.desc[blockIdx.x];
+    const Q4Desc d = q4_desc(jp.p.desc + blockIdx.x);
     if (d.pieces == 0) return;
     for (int r = tid / CH; r < d.rows; r += RPP)
-      q4_join_row<D>(jp.p, d, blockIdx.x, jp.p.part_ml, jp.p.part_o, jp.p.part_rows, r, ch);
+      q4_join_row<D, false>(jp.p, d, blockIdx.x, jp.p.part_ml, jp.p.part_o, jp.p.part_rows, r, tid % CH);
     return;
   }
   // the same list in every CTA: in the tiles' order
   static_assert(Q4_TC_MAX_CTAS <= 256, "a thread a descriptor");
-  const bool mine = tid < jp.tc && jp.tc_desc[tid].pieces > 0;
+  const bool mine = tid < jp.tc && __ldcg(&jp.tc_desc[tid].pieces) > 0;
   const unsigned votes = __ballot_sync(0xffffffffu, mine);
   if ((tid & 31) == 0) counts[tid >> 5] = __popc(votes);
   __syncthreads();
@@ -399,9 +421,9 @@ __global__ void __launch_bounds__(256) attend_q4_join_kernel(const Q4JoinParams 
   if (mine) list[before + __popc(votes & ((1u << (tid & 31)) - 1u))] = tid;
   __syncthreads();
   for (int item = blockIdx.x - jp.few; item < count * PARTS; item += gridDim.x - jp.few) {
-    const int cta = list[item / PARTS], r = item % PARTS * RPP + tid / CH;
-    const Q4Desc d = jp.tc_desc[cta];
-    if (r < d.rows) q4_join_row<D>(jp.p, d, cta, jp.tc_ml, jp.tc_o, jp.tc_rows, r, ch);
+    const int cta = list[item / PARTS], r = item % PARTS * RPP + tid % RPP;
+    const Q4Desc d = q4_desc(jp.tc_desc + cta);
+    if (r < d.rows) q4_join_row<D, true>(jp.p, d, cta, jp.tc_ml, jp.tc_o, jp.tc_rows, r, tid / RPP);
   }
 }
 

@@ -83,8 +83,8 @@ struct TqSmem {
   static constexpr uint32_t ZERO = KX + STAGES * 2048;              // ... and 8 of zeros behind either
   static constexpr uint32_t CODES = ZERO + 2048;                    // a step's K codes, and its V codes
   static constexpr uint32_t SC = CODES + 2 * STEP;                  // bf16 [SCS][128]: scales of the step's keys
-  static constexpr uint32_t ONES = SC + SCS * 256;                  // bf16 [128]: scales of scores that have theirs
-  static constexpr uint32_t BARS = ONES + 256;
+  static constexpr uint32_t ONES = SC + SCS * 512;                  // bf16 [128]: scales of scores that have theirs
+  static constexpr uint32_t BARS = ONES + 512;
   static constexpr uint32_t WALK = BARS + T_BARS * 8;               // TqPiece [2]
   static constexpr uint32_t META = WALK + 2 * sizeof(TqPiece);      // int [2][2], int [SCS], TMEM address, abort flag
   static constexpr uint32_t TOTAL = META + 4 * (4 + SCS + 2);
@@ -106,11 +106,6 @@ __device__ __forceinline__ void parts(f32x2 d, float& lo, float& hi) {
 __device__ __forceinline__ f32x2 fma2(f32x2 x, f32x2 y, f32x2 z) {
   f32x2 d;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
-  return d;
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 x, f32x2 y) {
-  f32x2 d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
   return d;
 }
 __device__ __forceinline__ f32x2 add2(f32x2 x, f32x2 y) {
@@ -174,7 +169,7 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (tid < 64) reinterpret_cast<uint32_t*>(sm + SM::ONES)[tid] = 0x3F803F80u;
+  if (tid < 128) reinterpret_cast<float*>(sm + SM::ONES)[tid] = 1.f;
   if (tid < 512) reinterpret_cast<uint32_t*>(sm + SM::ZERO)[tid] = 0u;
   fence_proxy_async_smem();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -416,7 +411,7 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
             const uint32_t r11 = pack_bf16(r, r);
             *reinterpret_cast<uint4*>(sm + SM::KX + sk * 2048 + t * 16) =
                 make_uint4(r11, pack_bf16(r, r2), pack_bf16(r2, r3), 0u);
-            reinterpret_cast<uint16_t*>(sm + SM::SC)[(n % SCS) * 128 + t] = (uint16_t)(__float_as_uint(s) >> 16);
+            reinterpret_cast<float*>(sm + SM::SC)[(n % SCS) * 128 + t] = s * p.scale_log2;
             if (t == 0) sc_ok[n % SCS] = there;
             mbar_arrive(&bars[T_SCFULL + n % SCS]);
           }
@@ -516,8 +511,7 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
             if (walk.piece < 0)
               q4_write_row<D>(p, walk.q0, rr, walk.h, ch, zero, -INFINITY, 0.f, ch == 0);
             else
-              *reinterpret_cast<float4*>(p.part_o + ((size_t)walk.piece * p.part_rows + half * 128 + row) * D + ch) =
-                  make_float4(0.f, 0.f, 0.f, 0.f);
+              *q4_tc_place<D>(p.part_o, p.part_rows, walk.piece, half * 128 + row, ch / 4) = make_float4(0.f, 0.f, 0.f, 0.f);
           }
           if (walk.piece >= 0) p.part_ml[(size_t)walk.piece * p.part_rows + half * 128 + row] = make_float2(-INFINITY, 0.f);
         }
@@ -530,8 +524,7 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
         wait(T_SFULL + half, used & 1);
         // (complete by now; waited for only after S, as this half may have skipped pieces and so completions)
         wait(T_SCFULL + n % SCS, (n / SCS) & 1);
-        const uint4* s8 = reinterpret_cast<const uint4*>(sm + SM::SC) + (n % SCS) * 16;   // scales of 8 keys
-        f32x2 c2 = pair(p.scale_log2, p.scale_log2);
+        const float4* s4 = reinterpret_cast<const float4*>(sm + SM::SC) + (n % SCS) * 32;   // of 4 keys: s * scale * log2 e
         const int ok = sc_ok[n % SCS];
         if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
         tc_fence_after();
@@ -544,7 +537,7 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
         // need be, and the maximum less itself is zero however large it is.
         bool careful = __any_sync(0xffffffffu, see < 128 || R == -INFINITY || fabsf(R) > 4096.f) || ok != 3;
         bool plain = true, passed = false;
-        // The halves take turns, so that one's pass runs beside the other's products; the turn is passed on after five
+        // The halves take turns, so that one's pass runs beside the other's products; the turn is passed on after six
         // of eight chunks (at the end: 716 us for the chunk of 4608 tokens, here 677, without turns 701).
         if (both && (half == 1 || turn > 0)) wait(T_TURN + (half ^ 1), (half == 1 ? turn : turn - 1) & 1);
 #pragma unroll 1
@@ -559,23 +552,20 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
               tmem_wait_ld();
               const int to = (ok >> (q >> 1)) & 1 ? see - q * 32 : 0;
 #pragma unroll
-              for (int e = 0; e < 32; e += 8) {
-                const uint4 s = s8[q * 4 + e / 8];
-                const uint32_t sw[4] = {s.x, s.y, s.z, s.w};
+              for (int e = 0; e < 32; e += 4) {
+                const float4 sc = s4[q * 8 + e / 4];
+                const float sw[4] = {sc.x, sc.y, sc.z, sc.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                  const float a = (__uint_as_float(x[e + 2 * i]) * lo_bf16(sw[i])) * p.scale_log2;
-                  const float b = (__uint_as_float(x[e + 2 * i + 1]) * hi_bf16(sw[i])) * p.scale_log2;
-                  x[e + 2 * i] = __float_as_uint(to <= e + 2 * i ? -INFINITY : a);
-                  x[e + 2 * i + 1] = __float_as_uint(to <= e + 2 * i + 1 ? -INFINITY : b);
-                  top = fmax3(top, __uint_as_float(x[e + 2 * i]), __uint_as_float(x[e + 2 * i + 1]));
+                  const float a = __uint_as_float(x[e + i]) * sw[i];
+                  x[e + i] = __float_as_uint(to <= e + i ? -INFINITY : a);
                 }
+                top = fmax3(fmax3(top, __uint_as_float(x[e]), __uint_as_float(x[e + 1])), __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
               }
               tmem_st32(tS + q * 32, x);
             }
             tmem_wait_st();
-            s8 = reinterpret_cast<const uint4*>(sm + SM::ONES);
-            c2 = pair(1.f, 1.f);
+            s4 = reinterpret_cast<const float4*>(sm + SM::ONES);
             if (R == -INFINITY || top > R + 64.f) R = top;
           }
           const float neg = R == -INFINITY ? 0.f : -R;
@@ -584,12 +574,12 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
           f32x2 sum0 = 0ull, sum1 = 0ull;
           uint32_t x[2][16];
           tmem_ld16(tS, x[0]);
-          uint4 sc[2][2];
-          sc[0][0] = s8[0];
-          sc[0][1] = s8[1];
+          float4 sc[2][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sc[0][i] = s4[i];
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
-            if (q == 5 && both && !passed) {
+            if (q == 6 && both && !passed) {
               passed = true;
               mbar_arrive(&bars[T_TURN + half]);
               ++turn;
@@ -597,18 +587,16 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
             tmem_wait16(x[q & 1]);
             if (q < 7) {
               tmem_ld16(tS + (q + 1) * 16, x[(q + 1) & 1]);   // in flight behind this chunk
-              sc[(q + 1) & 1][0] = s8[q * 2 + 2];
-              sc[(q + 1) & 1][1] = s8[q * 2 + 3];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) sc[(q + 1) & 1][i] = s4[q * 4 + 4 + i];
             }
 #pragma unroll
-            for (int e = 0; e < 16; e += 8) {
-              const uint4 s = sc[q & 1][e / 8];
-              const uint32_t sw[4] = {s.x, s.y, s.z, s.w};
+            for (int e = 0; e < 16; e += 4) {
+              const float4 s = sc[q & 1][e / 4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
+              for (int i = 0; i < 2; ++i) {
                 float y0, y1;
-                parts(fma2(mul2(pair(x[q & 1][e + 2 * i], x[q & 1][e + 2 * i + 1]), pair(sw[i] << 16, sw[i] & 0xFFFF0000u)),
-                           c2, neg2), y0, y1);
+                parts(fma2(pair(x[q & 1][e + 2 * i], x[q & 1][e + 2 * i + 1]), i ? pair(s.z, s.w) : pair(s.x, s.y), neg2), y0, y1);
                 if (i & 1) mx1 = fmax3(mx1, y0, y1);
                 else mx0 = fmax3(mx0, y0, y1);
                 y0 = ex2_approx(y0);
@@ -657,25 +645,34 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
         wait(T_MMADONE + half, done & 1);
         tc_fence_after();
         ++done;
+        const int tok = rr / p.group, head = walk.h * p.group + rr - tok * p.group;
+        const float inv = l == 0.f ? 0.f : 1.0f / l;   // a row without keys is zero
+        __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.o) + (long long)(walk.q0 + tok) * p.o_ld + (long long)head * D;
 #pragma unroll 1
         for (int q = 0; q < D / 32; ++q) {
           uint32_t ov[32];
           tmem_ld32(tO + q * 32, ov);
           tmem_wait_ld();
           if (live && !*abort_flag) {
+            if (walk.piece < 0) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const int ch = q * 32 + e;
-              const float acc[4] = {__uint_as_float(ov[e]), __uint_as_float(ov[e + 1]), __uint_as_float(ov[e + 2]),
-                                    __uint_as_float(ov[e + 3])};
-              if (walk.piece < 0)
-                q4_write_row<D>(p, walk.q0, rr, walk.h, ch, acc, M, l, ch == 0);
-              else
-                *reinterpret_cast<float4*>(p.part_o + ((size_t)walk.piece * p.part_rows + half * 128 + row) * D + ch) =
-                    make_float4(acc[0], acc[1], acc[2], acc[3]);
+              for (int e = 0; e < 32; e += 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  w[i] = pack_bf16(__uint_as_float(ov[e + 2 * i]) * inv, __uint_as_float(ov[e + 2 * i + 1]) * inv);
+                *reinterpret_cast<uint4*>(to + q * 32 + e) = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                *q4_tc_place<D>(p.part_o, p.part_rows, walk.piece, half * 128 + row, q * 8 + e / 4) =
+                    make_float4(__uint_as_float(ov[e]), __uint_as_float(ov[e + 1]), __uint_as_float(ov[e + 2]),
+                                __uint_as_float(ov[e + 3]));
             }
           }
         }
+        if (walk.piece < 0 && live && !*abort_flag && p.lse != nullptr) p.lse[(size_t)head * p.T + walk.q0 + tok] = q4_lse(M, l);
         if (walk.piece >= 0 && live && !*abort_flag)
           p.part_ml[(size_t)walk.piece * p.part_rows + half * 128 + row] = make_float2(M, l);
       }
