@@ -15,8 +15,9 @@
 //    noise into each):
 //      q . k = s (q . (c + 128) + (m / s - 128) sum(q)).
 //    The bracket is one product: (m / s - 128) and sum(q) as three bf16 terms each make a further slice of 16
-//    columns of K and Q.  The scale is applied to the scores in fp32; the softmax reads it as bf16, eight
-//    keys a load, since what every lane of a warp reads from shared memory costs as much as distinct data.
+//    columns of K and Q.  The scale, times the softmax scale, is applied to the scores in fp32, together with the
+//    subtraction of the reference: one multiply-add a pair.  (Read as bf16, half the shared-memory reads for three more
+//    instructions a pair, chunk and prompts took 2% and 4% longer.)
 //  * The halves take turns on the tensor pipe: while one's scores are exponentiated (a warpgroup each, a row
 //    a thread), the other's P V and next Q K^T run.  TMEM: S and O of each half (512 columns at D = 128), P as
 //    bf16 over S; S(i+1) is issued behind PV(i) by the half's own thread.
@@ -25,20 +26,22 @@
 //    scores exceed the reference by 2^64.  Above 2^8 the reference moves for the next step (O is rescaled then).
 //  * All barriers are used once per step with a step count that runs on over the pieces (a piece without
 //    blocks takes part in none; a half without rows in none of its own.  A thread that
-//    waits on a barrier waits on each of its completions, as a parity tells only neighbours apart).  The ring of key scales has four places:
-//    step n's are written once QK(n-2) is done, which follows the softmax of step n-3.
+//    waits on a barrier waits on each of its completions, as a parity tells only neighbours apart).  The ring of key
+//    scales has four places: step n's are written once QK(n-2) is done, which follows the softmax of step n-3.
 //  * Keys that a row does not see get x = -inf by a select after the scale is applied, and V of tokens
 //    that are not cached is zero, so whatever bytes lie there reach no row.
 // Waits are bounded; on expiry the error is recorded and every role runs through its pieces without
 // waiting, drains its copies and MMAs, frees TMEM and returns.
 //
-// Measured (D = 128): 4608 tokens of 12 heads over 13824, without the causal rule: 665-680 us, 575-590 TFLOP/s (0.34
-// of the measured 1685); three prompts of 700 .. 2048 tokens of 32 heads (8 kv heads) over 1000 .. 14000: 985-1008 us, 540
-// TFLOP/s.  A step of 256 rows and 128 keys lasts about 6400 cycles; its MMAs take 2800 of the tensor pipe's, its
+// Measured (D = 128): 4608 tokens of 12 heads over 13824, without the causal rule: 653-659 us, 595 TFLOP/s (0.35 of
+// the measured 1685); three prompts of 700 .. 2048 tokens of 32 heads (8 kv heads) over 1000 .. 14000: 944-952 us, 565
+// TFLOP/s.  A step of 256 rows and 128 keys lasts about 5900 cycles; its MMAs take 2800 of the tensor pipe's, its
 // exponentials 2048 of either unit's.  What bounds it is the chain of a half: a pass over 128 scores a thread (about
-// 3700 cycles, the unpacking and the other half in the same issue slots), then P V and the next Q K^T before S is there
-// again.  TMEM holds S and O of two halves and no third.  Tiles of 128 rows took 707 and 1168 us, two threads a row
-// 819 and 1219 (registers), the maximum found before the exponentials 799 and 1205.
+// 2900 cycles, the unpacking and the other half in the same issue slots), then 2300 until P V and the next Q K^T have
+// given the next S.  TMEM holds S and O of two halves and no third.  Earlier forms, when the chunk took 707 us and the
+// prompts 1168: two threads a row 819 and 1219 (registers), the maximum found before the exponentials 799 and 1205;
+// 256-row tiles then gave 701 and 1083.  A start and end of a tile cost about 12000 cycles.  A first reference of zero
+// instead of a first pass for the maximum: 668 and 966 us for 654 and 944; K unpacked before Q: 653 and 941.
 #include <math.h>
 
 #include "attend_q4.cuh"
@@ -82,8 +85,8 @@ struct TqSmem {
   static constexpr uint32_t KX = QX + 2 * 2048;                     // ... of each K stage
   static constexpr uint32_t ZERO = KX + STAGES * 2048;              // ... and 8 of zeros behind either
   static constexpr uint32_t CODES = ZERO + 2048;                    // a step's K codes, and its V codes
-  static constexpr uint32_t SC = CODES + 2 * STEP;                  // bf16 [SCS][128]: scales of the step's keys
-  static constexpr uint32_t ONES = SC + SCS * 512;                  // bf16 [128]: scales of scores that have theirs
+  static constexpr uint32_t SC = CODES + 2 * STEP;                  // float [SCS][128]: scales of the step's keys
+  static constexpr uint32_t ONES = SC + SCS * 512;                  // float [128]: of scores that have theirs
   static constexpr uint32_t BARS = ONES + 512;
   static constexpr uint32_t WALK = BARS + T_BARS * 8;               // TqPiece [2]
   static constexpr uint32_t META = WALK + 2 * sizeof(TqPiece);      // int [2][2], int [SCS], TMEM address, abort flag
@@ -538,7 +541,8 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
         bool careful = __any_sync(0xffffffffu, see < 128 || R == -INFINITY || fabsf(R) > 4096.f) || ok != 3;
         bool plain = true, passed = false;
         // The halves take turns, so that one's pass runs beside the other's products; the turn is passed on after six
-        // of eight chunks (at the end: 716 us for the chunk of 4608 tokens, here 677, without turns 701).
+        // of eight chunks (after four, five, six and seven the chunk of 4608 tokens takes 681, 675, 668 and 696 us, without
+        // turns 727).
         if (both && (half == 1 || turn > 0)) wait(T_TURN + (half ^ 1), (half == 1 ? turn : turn - 1) & 1);
 #pragma unroll 1
         while (true) {
