@@ -139,10 +139,11 @@ def test_captured_decode_step_follows_the_lengths():
     assert P.pbsa_get_device_error(s.batch.ws) == 0
 
 
-def test_two_graphs_with_workspaces_of_their_own_run_at_once():
+@pytest.mark.parametrize("heavy", [False, True])
+def test_two_graphs_with_workspaces_of_their_own_run_at_once(heavy):
     """Two captured attentions over the same cache, each with its own workspace, on two streams at the same time."""
     from tests._requests import Filled
-    f = Filled([(1, 9000), (2, 3000), (70, 500)], 4, 2, 128, "bf16", seed=21)
+    f = Filled([(1, 9000), (2, 3000), (70, 500)], 4, 2, 128, "bf16", seed=21, heavy=heavy)
     want, _ = f.attend(True)
     q = f.q.to(DEV)
     outs, graphs, streams = [], [], [torch.cuda.Stream() for _ in range(2)]
@@ -163,6 +164,39 @@ def test_two_graphs_with_workspaces_of_their_own_run_at_once():
     torch.cuda.synchronize()
     for o, ws in outs:
         assert torch.equal(o, want) and P.pbsa_get_device_error(ws) == 0
+
+
+def test_calls_one_after_another_share_a_workspace():
+    """Attentions that are much and little work, of many and of few rows, in turn over one workspace, eager and captured."""
+    from tests._requests import Filled
+    fs = [Filled([(1, 5000), (90, 300)], 4, 2, 128, "bf16", seed=23, heavy=True), Filled([(1, 700)] * 5, 8, 2, 128, "bf16", seed=24),
+          Filled([(200, 100), (3, 9)], 4, 2, 128, "bf16", seed=25), Filled([(20, 400)], 4, 2, 128, "f32", seed=26)]
+    want = [f.attend(True)[0] for f in fs]
+    for f in fs[1:]:
+        f.ws = fs[0].ws
+    qs = [f.q.to(DEV) for f in fs]
+    outs = [torch.zeros_like(w) for w in want]
+
+    def run():
+        for f, q, o in zip(fs, qs, outs):
+            P.pbsa_attend_q4(f.geom, q, f.q_start, f.q_len, f.kv_len, f.max_q, f.pool, f.slots, f.table, True, o, None, ws=f.ws)
+    run()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
+        o.zero_()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        run()
+        run()
+    for _ in range(10):
+        graph.replay()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
+    assert P.pbsa_get_device_error(fs[0].ws) == 0
 
 
 def test_a_stream_argument_is_used():
