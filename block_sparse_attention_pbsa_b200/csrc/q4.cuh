@@ -26,6 +26,10 @@
 
 namespace pbsa {
 
+// What rounds to infinity in bf16: half a step above its largest number (2^128 - 2^120), and more.  Held values end below,
+// or 0 * infinity would put NaN into rows that do not see the token.
+constexpr float Q4_PAST = 0x1.ffp127f;
+
 template <int D>
 struct Q4 {
   static constexpr int CODE = BT * D / 2;          // bytes of K (or V) codes of a slot

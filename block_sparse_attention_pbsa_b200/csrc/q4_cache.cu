@@ -4,9 +4,8 @@
 // quantised as q4.cuh defines and written to (head, slot, row).  One thread holds 16 neighbouring
 // channels (two or four 16-byte loads); the 8 (D = 64: 4) threads of a vector find its minimum and
 // maximum by shuffles, and a warp holds the K and the V of a token and head together, so that a
-// token whose K or V is not finite can be marked as one: its K scale and minimum become NaN (every
-// query that attends it then yields NaN) and its V zero, which keeps NaN out of the rows that
-// do not attend it.
+// token whose K or V is not finite, or would be read back as such, can be marked: its K scale and minimum become NaN
+// (every query that attends it then yields NaN) and its V zero, which keeps NaN out of the rows that do not attend it.
 // expand: s*c + m of every token of the listed slots, rounded once to the pools' type, in the
 // layout of the block pools that pbsa_attend reads.
 //
@@ -153,8 +152,8 @@ __global__ void __launch_bounds__(AP_THREADS) append_q4_kernel(const AppendParam
       const float span = __fsub_rn(hi, m);
       float s = bf16_up_pos(__fmul_rn(span, 1.0f / 15.0f));
       s = span == 0.f ? 0.f : fmaxf(s, 1.17549435e-38f);
-      // (NaN compares false: fmaxf would drop it, so the operands are tested themselves)
-      const bool bad = !(fabsf(lo) < INFINITY && fabsf(hi) < INFINITY && fabsf(m) < INFINITY && s < INFINITY);
+      // (NaN compares false: fmaxf would drop it, so the operands are tested themselves.  15 s + m bounds the values held.)
+      const bool bad = !(fabsf(lo) < INFINITY && fabsf(hi) < INFINITY && fabsf(m) < INFINITY && fmaf(15.f, s, m) < Q4_PAST);
       const unsigned votes = __ballot_sync(0xffffffffu, bad);
       const unsigned pair = (2 * LPV == 32 ? 0xffffffffu : ((1u << (2 * LPV)) - 1u)) << (sub * 2 * LPV);
       const bool poison = (votes & pair) != 0;

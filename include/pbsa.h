@@ -338,8 +338,9 @@ PBSA_API pbsa_status pbsa_memory_update_noalloc(const pbsa_geom* g, const float*
  *   m = the largest bf16 <= min x,  s = the smallest bf16 >= (max x - m) / 15 (0 if max x = m, else
  *   >= 2^-126),  c_i = round((x_i - m) / s) in 0 .. 15 (ties to even),  and stand for  s*c_i + m
  * ((max x - m) / 15 and (x_i - m) / s are fp32 products with the fp32 1/15 and 1/s).  A token whose K
- * or V of a head holds a value that is not finite, or a range above fp32's or bf16's, has NaN as that
- * head's K and zero as its V: queries that attend it yield NaN, others are not touched by it.
+ * or V of a head holds a value that is not finite, or has an m, a range max x - m or a 15 s + m that
+ * bf16 or fp32 would round to infinity, has NaN as that head's K and zero as its V: queries that attend
+ * it yield NaN, others are not touched by it.
  * The fields' order inside a slot is the library's own: pbsa_append_q4 alone writes it, pbsa_expand_q4
  * reads it back.  Workspaces are 16-byte aligned where they are given.
  *

@@ -77,8 +77,16 @@ def quantise(x):
 
 def held(k, v):
     """The values that the cache holds for k, v [..., d], float64: a token and head with a value that is not
-    finite in k or v holds NaN as k and 0 as v."""
+    finite in k or v, or whose minimum, range or uppermost held value bf16 or fp32 would round to infinity, holds
+    NaN as k and 0 as v."""
     bad = ~(np.isfinite(k).all(-1, keepdims=True) & np.isfinite(v).all(-1, keepdims=True))
+    past = 2.0 ** 128 - 2.0 ** 119                       # half a step above bf16's largest number, 2^128 - 2^120
+    for x in (k, v):
+        x = np.where(bad, 0.0, x)
+        lo, hi = x.min(-1, keepdims=True), x.max(-1, keepdims=True)
+        wide = (_bf16_side(lo, False) < -past) | (hi - _bf16_side(lo, False) >= 2.0 ** 128 - 2.0 ** 103)
+        _, s, m = quantise(np.where(wide, 0.0, x))
+        bad = bad | wide | (_f32(np.minimum(15.0 * s + m, past)) >= past)
     out = []
     for x, mark in ((k, np.nan), (v, 0.0)):
         c, s, m = quantise(np.where(bad, 0.0, x))
