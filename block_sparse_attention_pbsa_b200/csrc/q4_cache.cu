@@ -284,8 +284,10 @@ cudaError_t append_u(const AppendParams& p, cudaStream_t st) {
 
 template <typename T, int D>
 cudaError_t append_t(const AppendParams& p, cudaStream_t st) {
-  // a few items are spread over warps, many are loaded four at a time
-  return (long long)p.T * p.H < 16384 ? append_u<T, D, 1>(p, st) : append_u<T, D, 2>(p, st);
+  // Few items are spread over as many warps as there are, many go in pairs.  Singly and in pairs, bf16 of D = 128: 512
+  // items 2.3 and 2.6 us, 2048 2.9 and 2.6, 4096 3.4 and 2.9, 16384 6.6 and 4.3, 55296 15.1 and 10.0; fp32 of D = 128,
+  // the last to gain: 2048 2.7 and 2.7, 3072 2.9 and 3.1, 4096 3.1 and 3.1, 8192 4.2 and 3.9, 16384 6.7 and 5.1.
+  return (long long)p.T * p.H < 4096 ? append_u<T, D, 1>(p, st) : append_u<T, D, 2>(p, st);
 }
 
 }  // namespace
