@@ -36,6 +36,24 @@ def _on(stream):
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
+def _saved(owner, config: dict, device) -> dict:
+    st = {name: getattr(owner, name).to(device, copy=True) for name in owner._STATE}
+    return {**st, "config": config}
+
+
+def _load(owner, st: dict, config: dict):
+    """All of a state, or nothing where any of it does not fit."""
+    what = type(owner).__name__
+    if st.get("config") != config:
+        raise ValueError(f"the state was taken from a {what} of another configuration")
+    for name in owner._STATE:
+        dst, src = getattr(owner, name), st.get(name)
+        if not isinstance(src, torch.Tensor) or src.shape != dst.shape or src.dtype != dst.dtype:
+            raise ValueError(f"{name}: shape or dtype does not match the {what}")
+    for name in owner._STATE:
+        getattr(owner, name).copy_(st[name])
+
+
 class RequestBatch:
     def __init__(self, cfg: RequestConfig, device="cuda"):
         self.cfg = cfg
@@ -78,17 +96,13 @@ class RequestBatch:
     _STATE = ("kv_len", "block_table", "free_slot", "free_cnt")
 
     def state_dict(self, device="cpu") -> dict:
-        """Everything that the next step needs (copied to ``device``)."""
-        st = {name: getattr(self, name).to(device, copy=True) for name in self._STATE}
-        st["config"] = dataclasses.asdict(self.cfg)
-        return st
+        """The lengths, block tables and free slots (copied to ``device``).  With the
+        ``state_dict`` of each layer's cache, which holds the K and V, it is everything that the next step needs."""
+        return _saved(self, dataclasses.asdict(self.cfg), device)
 
     def load_state_dict(self, st: dict):
         """Restore a ``state_dict`` of a batch of the same configuration."""
-        if st.get("config") != dataclasses.asdict(self.cfg):
-            raise ValueError("the state was taken from a batch of another configuration")
-        for name in self._STATE:
-            getattr(self, name).copy_(st[name])
+        _load(self, st, dataclasses.asdict(self.cfg))
 
 
 class Q4LayerCache:
@@ -144,3 +158,19 @@ class Q4LayerCache:
                 v_pool = torch.zeros(shape, dtype=dt, device=self.batch.device) if v_pool is None else v_pool
         L.pbsa_expand_q4(self.geom, self.pool, self.batch.cfg.pool_slots, slots, k_pool, v_pool, ws=self.ws, stream=stream)
         return k_pool, v_pool
+
+    # ------------------------------------------------------------------ checkpoint / resume
+    _STATE = ("pool",)
+
+    def _config(self) -> dict:
+        g = self.geom
+        return dict(q_heads=g.q_heads, kv_heads=g.kv_heads, head_dim=g.head_dim, scale=g.scale, dtype=g.dtype,
+                    pool_slots=self.batch.cfg.pool_slots)
+
+    def state_dict(self, device="cpu") -> dict:
+        """The cached K and V (copied to ``device``), beside the batch's own state."""
+        return _saved(self, self._config(), device)
+
+    def load_state_dict(self, st: dict):
+        """Restore a ``state_dict`` of a cache of the same heads, head size, scale, type and number of slots."""
+        _load(self, st, self._config())

@@ -1,0 +1,49 @@
+"""A batch saved with its caches and resumed in new ones; steps whose numbers the host does not see."""
+import pytest
+import torch
+
+import block_sparse_attention_pbsa_b200 as P
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+CFG = P.RequestConfig(requests=3, blocks=4, tokens=100, pool_slots=8)
+
+
+def _step(batch, cache, step, seed):
+    gen = torch.Generator().manual_seed(seed)
+    q, k, v = (torch.randn((CFG.tokens, h, 64), generator=gen).to(torch.bfloat16).to(DEV) for h in (4, 2, 2))
+    batch.step(step, max(step))
+    cache.append(k, v)
+    return cache.attend(q)
+
+
+def test_a_resumed_batch_attends_as_the_one_that_ran_on():
+    a = P.RequestBatch(CFG)
+    ca = P.Q4LayerCache(a, 4, 2, 64)
+    _step(a, ca, [70, 1, 29], 1)
+    saved = a.state_dict(), ca.state_dict()
+    b = P.RequestBatch(CFG)
+    cb = P.Q4LayerCache(b, 4, 2, 64)
+    b.load_state_dict(saved[0])
+    cb.load_state_dict(saved[1])
+    for seed, step in ((2, [1, 1, 1]), (3, [-1, 64, 30])):
+        assert torch.equal(_step(a, ca, step, seed), _step(b, cb, step, seed))
+    for cache in (ca, cb):
+        assert P.pbsa_get_device_error(cache.ws) == 0
+
+
+def test_states_of_other_caches_are_refused():
+    a = P.RequestBatch(CFG)
+    st = P.Q4LayerCache(a, 4, 2, 64).state_dict()
+    for other in (P.Q4LayerCache(a, 4, 1, 64), P.Q4LayerCache(a, 4, 2, 128), P.Q4LayerCache(a, 4, 2, 64, dtype="f32"),
+                  P.Q4LayerCache(P.RequestBatch(P.RequestConfig(3, 4, 100, 9)), 4, 2, 64)):
+        before = other.pool.clone()
+        with pytest.raises(ValueError):
+            other.load_state_dict(st)
+        assert torch.equal(other.pool, before)
+    bst = a.state_dict()
+    bst["free_slot"] = bst["free_slot"][:3]
+    before = a.state_dict()
+    with pytest.raises(ValueError):
+        a.load_state_dict(bst)
+    assert all(torch.equal(before[n], a.state_dict()[n]) for n in ("kv_len", "block_table", "free_slot", "free_cnt"))
