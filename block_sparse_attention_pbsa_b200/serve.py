@@ -87,10 +87,10 @@ class RequestBatch:
                 raise ValueError(f"step_len must have {self.cfg.requests} entries, got {list(step_len.shape)}")
             with _on(stream):
                 self.step_len.copy_(step_len)
-        self.max_q_len = max_q_len
         L.pbsa_request_tables(self.step_len, self.kv_len, self.block_table, self.free_slot, self.free_cnt, self.q_start,
                               self.q_len, self.kv_len, self.free_cnt, self.slot_map, self.position, ws=self.ws,
                               stream=stream)
+        self.max_q_len = max_q_len
 
     # ------------------------------------------------------------------ checkpoint / resume
     _STATE = ("kv_len", "block_table", "free_slot", "free_cnt")
@@ -101,8 +101,14 @@ class RequestBatch:
         return _saved(self, dataclasses.asdict(self.cfg), device)
 
     def load_state_dict(self, st: dict):
-        """Restore a ``state_dict`` of a batch of the same configuration."""
+        """Restore a ``state_dict`` of a batch of the same configuration.  The batch is then between two steps: until
+        the next one no row has a place in the cache and no request has tokens."""
         _load(self, st, dataclasses.asdict(self.cfg))
+        for t in (self.step_len, self.q_start, self.q_len):
+            t.zero_()
+        for t in (self.slot_map, self.position):
+            t.fill_(-1)
+        self.max_q_len = 0
 
 
 class Q4LayerCache:

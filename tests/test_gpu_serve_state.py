@@ -32,6 +32,21 @@ def test_a_resumed_batch_attends_as_the_one_that_ran_on():
         assert P.pbsa_get_device_error(cache.ws) == 0
 
 
+def test_a_loaded_state_has_no_step_yet():
+    """What the target's own last step left does not go on: nothing is written or attended before the next step."""
+    a, b = P.RequestBatch(CFG), P.RequestBatch(CFG)
+    ca, cb = P.Q4LayerCache(a, 4, 2, 64), P.Q4LayerCache(b, 4, 2, 64)
+    _step(a, ca, [70, 1, 29], 1)
+    _step(b, cb, [1, 90, 2], 2)
+    b.load_state_dict(a.state_dict())
+    cb.load_state_dict(ca.state_dict())
+    x = torch.ones((CFG.tokens, 4, 64), dtype=torch.bfloat16, device=DEV)
+    cb.append(x[:, :2], x[:, 2:])
+    assert torch.equal(cb.pool, ca.pool)
+    assert (cb.attend(x) == 0).all()
+    assert (b.slot_map == -1).all() and (b.position == -1).all() and (b.q_len == 0).all() and b.max_q_len == 0
+
+
 def test_states_of_other_caches_are_refused():
     a = P.RequestBatch(CFG)
     st = P.Q4LayerCache(a, 4, 2, 64).state_dict()

@@ -21,9 +21,15 @@ def test_states_are_copies_and_come_back_whole():
     c.pool.zero_()
     assert saved[0]["kv_len"].tolist() == [5, 0, 70] and torch.equal(saved[1]["pool"], bytes_)
     b2, c2 = _pair()
+    for t in (b2.q_len, b2.slot_map, b2.position, b2.q_start, b2.step_len):
+        t.fill_(3)
+    b2.max_q_len = 3
     b2.load_state_dict(saved[0])
     c2.load_state_dict(saved[1])
     assert b2.kv_len.tolist() == [5, 0, 70] and torch.equal(c2.pool, bytes_)
+    # between two steps
+    assert (b2.slot_map == -1).all() and (b2.position == -1).all() and b2.max_q_len == 0
+    assert not b2.q_len.any() and not b2.q_start.any() and not b2.step_len.any()
 
 
 def test_a_state_that_does_not_fit_changes_nothing():
@@ -39,3 +45,11 @@ def test_a_state_that_does_not_fit_changes_nothing():
             P.Q4LayerCache(b, *args).load_state_dict(c.state_dict())
     with pytest.raises(ValueError):
         c.load_state_dict(b.state_dict())
+
+
+def test_a_step_that_is_refused_keeps_the_bound():
+    b, _ = _pair()
+    b.max_q_len = 2
+    with pytest.raises((ValueError, RuntimeError)):
+        b.step([1, 1, 1], 1)                 # the tables are on the CPU
+    assert b.max_q_len == 2
