@@ -36,12 +36,13 @@ def _on(stream):
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
-def _saved(owner, config: dict, device) -> dict:
-    st = {name: getattr(owner, name).to(device, copy=True) for name in owner._STATE}
+def _saved(owner, config: dict, device, stream) -> dict:
+    with _on(stream):
+        st = {name: getattr(owner, name).to(device, copy=True) for name in owner._STATE}
     return {**st, "config": config}
 
 
-def _load(owner, st: dict, config: dict):
+def _load(owner, st: dict, config: dict, stream):
     """All of a state, or nothing where any of it does not fit."""
     what = type(owner).__name__
     if st.get("config") != config:
@@ -50,8 +51,9 @@ def _load(owner, st: dict, config: dict):
         dst, src = getattr(owner, name), st.get(name)
         if not isinstance(src, torch.Tensor) or src.shape != dst.shape or src.dtype != dst.dtype:
             raise ValueError(f"{name}: shape or dtype does not match the {what}")
-    for name in owner._STATE:
-        getattr(owner, name).copy_(st[name])
+    with _on(stream):
+        for name in owner._STATE:
+            getattr(owner, name).copy_(st[name])
 
 
 class RequestBatch:
@@ -95,19 +97,20 @@ class RequestBatch:
     # ------------------------------------------------------------------ checkpoint / resume
     _STATE = ("kv_len", "block_table", "free_slot", "free_cnt")
 
-    def state_dict(self, device="cpu") -> dict:
-        """The lengths, block tables and free slots (copied to ``device``).  With the
+    def state_dict(self, device="cpu", stream=None) -> dict:
+        """The lengths, block tables and free slots (copied to ``device`` on ``stream``, that of the steps).  With the
         ``state_dict`` of each layer's cache, which holds the K and V, it is everything that the next step needs."""
-        return _saved(self, dataclasses.asdict(self.cfg), device)
+        return _saved(self, dataclasses.asdict(self.cfg), device, stream)
 
-    def load_state_dict(self, st: dict):
+    def load_state_dict(self, st: dict, stream=None):
         """Restore a ``state_dict`` of a batch of the same configuration.  The batch is then between two steps: until
         the next one no row has a place in the cache and no request has tokens."""
-        _load(self, st, dataclasses.asdict(self.cfg))
-        for t in (self.step_len, self.q_start, self.q_len):
-            t.zero_()
-        for t in (self.slot_map, self.position):
-            t.fill_(-1)
+        _load(self, st, dataclasses.asdict(self.cfg), stream)
+        with _on(stream):
+            for t in (self.step_len, self.q_start, self.q_len):
+                t.zero_()
+            for t in (self.slot_map, self.position):
+                t.fill_(-1)
         self.max_q_len = 0
 
 
@@ -173,10 +176,10 @@ class Q4LayerCache:
         return dict(q_heads=g.q_heads, kv_heads=g.kv_heads, head_dim=g.head_dim, scale=g.scale, dtype=g.dtype,
                     pool_slots=self.batch.cfg.pool_slots)
 
-    def state_dict(self, device="cpu") -> dict:
-        """The cached K and V (copied to ``device``), beside the batch's own state."""
-        return _saved(self, self._config(), device)
+    def state_dict(self, device="cpu", stream=None) -> dict:
+        """The cached K and V (copied to ``device`` on ``stream``, that of the steps), beside the batch's own state."""
+        return _saved(self, self._config(), device, stream)
 
-    def load_state_dict(self, st: dict):
+    def load_state_dict(self, st: dict, stream=None):
         """Restore a ``state_dict`` of a cache of the same heads, head size, scale, type and number of slots."""
-        _load(self, st, self._config())
+        _load(self, st, self._config(), stream)

@@ -47,6 +47,34 @@ def test_a_loaded_state_has_no_step_yet():
     assert (b.slot_map == -1).all() and (b.position == -1).all() and (b.q_len == 0).all() and b.max_q_len == 0
 
 
+def test_a_state_is_taken_on_the_stream_of_its_steps():
+    a = P.RequestBatch(CFG)
+    ca = P.Q4LayerCache(a, 4, 2, 64)
+    x = torch.ones((CFG.tokens, 4, 64), dtype=torch.bfloat16, device=DEV)
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        torch.cuda._sleep(20_000_000)
+    a.step(torch.tensor([70, 1, 29], dtype=torch.int32, device=DEV), 70, stream=st)
+    ca.append(x[:, :2], x[:, 2:], stream=st)
+    saved = a.state_dict(stream=st), ca.state_dict(stream=st)
+    torch.cuda.synchronize()
+    assert saved[0]["kv_len"].tolist() == [70, 1, 29] and torch.equal(saved[1]["pool"], ca.pool.cpu())
+    b = P.RequestBatch(CFG)
+    cb = P.Q4LayerCache(b, 4, 2, 64)
+    with torch.cuda.stream(st):
+        torch.cuda._sleep(20_000_000)
+    b.load_state_dict(saved[0], stream=st)
+    cb.load_state_dict(saved[1], stream=st)
+    o = torch.zeros_like(x)
+    b.step([1, 1, 1], 1, stream=st)
+    cb.attend(x, o=o, stream=st)
+    a.step([1, 1, 1], 1, stream=st)
+    want = ca.attend(x, stream=st)
+    torch.cuda.synchronize()
+    assert torch.equal(b.kv_len, a.kv_len) and torch.equal(o, want)
+
+
 def test_states_of_other_caches_are_refused():
     a = P.RequestBatch(CFG)
     st = P.Q4LayerCache(a, 4, 2, 64).state_dict()
