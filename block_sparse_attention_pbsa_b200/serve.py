@@ -76,7 +76,8 @@ class RequestBatch:
     def step(self, step_len, max_q_len: int, stream=None):
         """The tables of a step: request r adds ``step_len[r]`` tokens (0: none, negative: it has ended and its
         blocks are free again).  ``step_len`` is a device tensor (None: what ``self.step_len`` holds, as in a captured
-        step) or a list; no entry is above ``max_q_len``.  Afterwards ``q_len`` tells which requests were served
+        step) or a list; no entry is above ``max_q_len`` (a tensor's are not looked at here: the attention leaves such a
+        request out and records it, see ``Q4LayerCache``).  Afterwards ``q_len`` tells which requests were served
         (a request that found no room has 0), ``slot_map`` and ``position`` where the step's tokens go."""
         if not 0 <= max_q_len <= self.cfg.tokens:
             raise ValueError(f"max_q_len must lie in [0, {self.cfg.tokens}], got {max_q_len}")
@@ -116,7 +117,9 @@ class RequestBatch:
 
 class Q4LayerCache:
     """One layer's 4-bit pool for the requests of ``batch``.  ``ws`` may be shared by the layers of a model, whose
-    calls follow one another (see pbsa_attend_q4_workspace_bytes)."""
+    calls follow one another (see pbsa_attend_q4_workspace_bytes).  What the calls find wrong on the device -- slots
+    outside the pool, requests whose numbers are out of range -- is in the error words of ``ws`` and ``batch.ws``, which
+    ``pbsa_get_device_error`` reads and clears."""
 
     def __init__(self, batch: RequestBatch, q_heads: int, kv_heads: int, head_dim: int, dtype="bf16", scale=None, ws=None):
         self.batch = batch

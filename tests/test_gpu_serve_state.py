@@ -90,3 +90,16 @@ def test_states_of_other_caches_are_refused():
     with pytest.raises(ValueError):
         a.load_state_dict(bst)
     assert all(torch.equal(before[n], a.state_dict()[n]) for n in ("kv_len", "block_table", "free_slot", "free_cnt"))
+
+
+def test_an_entry_above_the_bound_is_recorded():
+    """A tensor's entries are not looked at on the host: a request above max_q_len is left out of the attention, which
+    the layer's error word tells."""
+    a = P.RequestBatch(CFG)
+    c = P.Q4LayerCache(a, 4, 2, 64)
+    x = torch.ones((CFG.tokens, 4, 64), dtype=torch.bfloat16, device=DEV)
+    a.step(torch.tensor([5, 2, 0], dtype=torch.int32), 4)
+    c.append(x[:, :2], x[:, 2:])
+    o = c.attend(x)
+    assert (o[:5] == 0).all() and (o[5:7] != 0).all()
+    assert P.pbsa_get_device_error(a.ws) == 0 and P.pbsa_get_device_error(c.ws) == 5
