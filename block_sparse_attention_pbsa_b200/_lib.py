@@ -9,7 +9,9 @@ kernels; there is no fallback of any kind -- if the library is missing or was no
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
+import sysconfig
 
 import torch
 
@@ -104,7 +106,7 @@ OPTIONAL = {}
 
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load libpbsa.so (raises if it is absent: there is no fallback path)."""
-    global _lib, _binding
+    global _lib
     if _lib is not None:
         return _lib
     if not os.path.exists(path):
@@ -118,15 +120,6 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             continue
         f = getattr(lib, name)
         f.restype, f.argtypes = res, args
-    try:
-        from . import _requests as binding
-    except ImportError as e:
-        raise RuntimeError(f"the binding _requests.so cannot be imported ({e}); build it with "
-                           "`python -m block_sparse_attention_pbsa_b200.build`") from e
-    binding.bind(*(ctypes.cast(getattr(lib, name), _P).value for name in (
-        "pbsa_request_tables", "pbsa_append_q4", "pbsa_expand_q4", "pbsa_attend_q4", "pbsa_q4_block_bytes",
-        "pbsa_attend_q4_workspace_bytes")))
-    _binding = binding
     _lib = lib
     return lib
 
@@ -329,8 +322,27 @@ def pbsa_attend_q4_workspace_bytes(g: ReqGeom) -> int:
 # These calls are made per layer and step: their arguments are checked in requests_binding.cpp, which raises ValueError
 # for tensors of another device, type, shape or layout than the call takes.
 
+def binding_path() -> str:
+    """Where the binding for this interpreter and this torch lies: it fits no other."""
+    return os.path.join(_PKG, f"_requests-{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
 def _requests():
-    load()
+    """The binding, loaded on first use: no other call needs it."""
+    global _binding
+    if _binding is None:
+        lib = load()
+        spec = importlib.util.spec_from_file_location(__package__ + "._requests", binding_path())
+        try:
+            binding = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(binding)
+        except ImportError as e:
+            raise RuntimeError(f"the binding of the request calls cannot be imported ({e}); build it with "
+                               "`python -m block_sparse_attention_pbsa_b200.build`") from e
+        binding.bind(*(ctypes.cast(getattr(lib, f), _P).value for f in (
+            "pbsa_request_tables", "pbsa_append_q4", "pbsa_expand_q4", "pbsa_attend_q4", "pbsa_q4_block_bytes",
+            "pbsa_attend_q4_workspace_bytes")))
+        _binding = binding
     return _binding
 
 
