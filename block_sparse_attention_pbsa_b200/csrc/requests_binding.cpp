@@ -46,6 +46,18 @@ struct Env {
       stream = c10::cuda::getCurrentCUDAStream(index).stream();
       return;
     }
+    // a launch on another device's stream fails, or runs there on this device's memory
+    PyObject* d = PyObject_GetAttrString(s, "device_index");
+    if (d != nullptr) {
+      const long at = PyLong_AsLong(d);
+      Py_DECREF(d);
+      if (at == -1 && PyErr_Occurred()) throw Raised();
+      if (at != index) throw Refused("stream must be one of the current CUDA device");
+    } else if (PyErr_ExceptionMatches(PyExc_AttributeError)) {
+      PyErr_Clear();   // a stream of another library, which does not tell
+    } else {
+      throw Raised();
+    }
     PyObject* h = PyObject_GetAttrString(s, "cuda_stream");
     if (h == nullptr) throw Raised();
     stream = PyLong_AsVoidPtr(h);

@@ -103,3 +103,24 @@ def test_an_entry_above_the_bound_is_recorded():
     o = c.attend(x)
     assert (o[:5] == 0).all() and (o[5:7] != 0).all()
     assert P.pbsa_get_device_error(a.ws) == 0 and P.pbsa_get_device_error(c.ws) == 5
+
+
+def test_a_stream_of_another_device_is_refused():
+    class Elsewhere:
+        cuda_stream, device_index = 0, torch.cuda.current_device() + 1
+
+    a = P.RequestBatch(CFG)
+    c = P.Q4LayerCache(a, 4, 2, 64)
+    x = torch.ones((CFG.tokens, 4, 64), dtype=torch.bfloat16, device=DEV)
+    slots = torch.zeros(1, dtype=torch.int32, device=DEV)
+    kv = torch.zeros((2, 1, 64, 64), dtype=torch.bfloat16, device=DEV)
+    s = Elsewhere()
+    for call in (
+            lambda: P.pbsa_request_tables(a.step_len, a.kv_len, a.block_table, a.free_slot, a.free_cnt, a.q_start, a.q_len,
+                                          a.kv_len, a.free_cnt, a.slot_map, stream=s),
+            lambda: P.pbsa_append_q4(c.geom, x[:, :2], x[:, 2:], a.slot_map, c.pool, CFG.pool_slots, stream=s),
+            lambda: P.pbsa_expand_q4(c.geom, c.pool, CFG.pool_slots, slots, kv, kv.clone(), stream=s),
+            lambda: P.pbsa_attend_q4(c.geom, x, a.q_start, a.q_len, a.kv_len, 1, c.pool, CFG.pool_slots, a.block_table, True,
+                                     torch.zeros_like(x), ws=c.ws, stream=s)):
+        with pytest.raises(ValueError, match="stream"):
+            call()
