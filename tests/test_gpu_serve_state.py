@@ -1,4 +1,5 @@
-"""A batch saved with its caches and resumed in new ones; steps whose numbers the host does not see."""
+"""A batch saved with its caches and resumed in new ones; steps whose numbers the host does not see; streams and
+tensors of another place; captured attentions that overlap."""
 import pytest
 import torch
 
@@ -124,3 +125,45 @@ def test_a_stream_of_another_device_is_refused():
                                      torch.zeros_like(x), ws=c.ws, stream=s)):
         with pytest.raises(ValueError, match="stream"):
             call()
+
+
+def test_the_binding_names_what_lies_on_the_host():
+    """The refusals are the binding's own, not torch's."""
+    g = P.make_req_geom(2, 2, 64, 0.1, "bf16")
+    x = torch.zeros((4, 2, 64), dtype=torch.bfloat16)
+    i, pool = torch.zeros(4, dtype=torch.int32), torch.zeros(2 * 3 * 4608, dtype=torch.uint8)
+    dev = lambda *t: [y.to(DEV) for y in t]  # noqa: E731
+    for name, args in (("k", (x, *dev(x, i, pool))), ("v", (*dev(x), x, *dev(i, pool))), ("slot_map", (*dev(x, x), i, *dev(pool))),
+                       ("pool", (*dev(x, x, i), pool))):
+        with pytest.raises(ValueError, match=f"^{name} must be a tensor of the current CUDA device"):
+            P.pbsa_append_q4(g, *args, 3)
+
+
+@pytest.mark.parametrize("heavy", [False, True])
+def test_every_replay_of_two_graphs_at_once_gives_the_same(heavy):
+    """Two captured attentions with workspaces of their own on two streams: the outputs of each of the replays are kept."""
+    from tests._requests import Filled
+    f = Filled([(1, 9000), (2, 3000), (70, 500)], 4, 2, 128, "bf16", seed=21, heavy=heavy)
+    want, wl = f.attend(True)
+    q, runs, streams = f.q.to(DEV), [], [torch.cuda.Stream() for _ in range(2)]
+    for st in streams:
+        ws, o, lse = torch.zeros_like(f.ws), torch.zeros_like(want), torch.zeros_like(wl)
+        st.wait_stream(torch.cuda.current_stream())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            P.pbsa_attend_q4(f.geom, q, f.q_start, f.q_len, f.kv_len, f.max_q, f.pool, f.slots, f.table, True, o, lse, ws=ws)
+        runs.append((g, o, lse, ws, torch.zeros((20, *o.shape), dtype=o.dtype, device=DEV), torch.zeros((20, *lse.shape), device=DEV)))
+    torch.cuda.synchronize()
+    for i in range(20):
+        for st, (g, o, lse, _, keep_o, keep_l) in zip(streams, runs):
+            with torch.cuda.stream(st):
+                o.zero_()
+                lse.zero_()
+                g.replay()
+                keep_o[i].copy_(o)
+                keep_l[i].copy_(lse)
+    torch.cuda.synchronize()
+    for _, _, _, ws, keep_o, keep_l in runs:
+        for i in range(20):
+            assert torch.equal(keep_o[i], want) and torch.equal(keep_l[i], wl), i
+        assert P.pbsa_get_device_error(ws) == 0
