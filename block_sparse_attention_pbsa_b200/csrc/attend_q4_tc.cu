@@ -10,8 +10,8 @@
 //    beside the few-rows kernel's last CTAs, from which it reads nothing.
 //  * Each step covers two blocks (128 keys).  One thread each brings K's and V's bytes with bulk copies;
 //    two warpgroups, alternate steps, unpack them into shared-memory operand tiles (128-byte swizzle): K as
-//    the codes themselves (plus 128, exact in bf16), V as bf16 values s*c + m, rounded once, the bits that
-//    pbsa_expand_q4 gives.  The scores carry no rounding of K (to bf16 it would put 2^-8 |q . k| / sqrt(d) of
+//    the codes themselves (plus 128, exact in bf16), V as bf16 values s*c + m, rounded once (pbsa_expand_q4 rounds to fp32
+//    first, so a value next to the middle of two bf16 numbers may differ by a step).  The scores carry no rounding of K (to bf16 it would put 2^-8 |q . k| / sqrt(d) of
 //    noise into each):
 //      q . k = s (q . (c + 128) + (m / s - 128) sum(q)).
 //    The bracket is one product: (m / s - 128) and sum(q) as three bf16 terms each make a further slice of 16

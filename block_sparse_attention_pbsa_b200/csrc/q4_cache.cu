@@ -6,8 +6,8 @@
 // maximum by shuffles, and a warp holds the K and the V of a token and head together, so that a
 // token whose K or V is not finite, or would be read back as such, can be marked: its K scale and minimum become NaN
 // (every query that attends it then yields NaN) and its V zero, which keeps NaN out of the rows that do not attend it.
-// expand: s*c + m of every token of the listed slots, rounded once to the pools' type, in the
-// layout of the block pools that pbsa_attend reads.
+// expand: s*c + m of every token of the listed slots, rounded to fp32 and, where that is the pools' type, from there to
+// bf16, in the layout of the block pools that pbsa_attend reads.
 //
 // append reads 2*D*sizeof(T) bytes and writes D + 8 per (token, head): 36 MB, 5.5 us, for 4608 tokens of 12
 // heads, which take 10.1 us (3.6 TB/s).  It is bound by issue: about 130 warp instructions a token and head, most

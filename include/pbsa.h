@@ -400,8 +400,8 @@ PBSA_API pbsa_status pbsa_append_q4(const pbsa_req_geom* g, const void* k, long 
                            long long v_ld, int n_tokens, const int* slot_map, void* pool, int pool_slots, void* ws,
                            void* stream);
 
-/* Slots of the 4-bit pool as dense blocks: s*c + m, rounded to the geometry's dtype, of all 64 tokens of
- * slot src_slot[i] into block i of k_pool and v_pool [kv_heads][n_slots][64][d] -- pools as pbsa_attend
+/* Slots of the 4-bit pool as dense blocks: s*c + m, rounded to fp32 (and for PBSA_BF16 from there to bf16), of all
+ * 64 tokens of slot src_slot[i] into block i of k_pool and v_pool [kv_heads][n_slots][64][d] -- pools as pbsa_attend
  * reads.  src_slot[i] = -1 leaves block i as it is; another id outside the pool does too and is recorded. */
 PBSA_API pbsa_status pbsa_expand_q4(const pbsa_req_geom* g, const void* pool, int pool_slots, const int* src_slot,
                            int n_slots, void* k_pool, void* v_pool, void* ws, void* stream);
@@ -411,6 +411,11 @@ PBSA_API pbsa_status pbsa_expand_q4(const pbsa_req_geom* g, const void* pool, in
  * over the first kv_len[r] tokens of its table row; with PBSA_CAUSAL over the first
  * kv_len[r] - q_len[r] + i + 1 (the step's tokens are the cache's last).  k_j, v_j are the values that the
  * pool holds.  A token without keys gives o = 0 and lse = -inf.
+ * Sums are fp32.  With PBSA_BF16 the products take weights rounded to bf16, and requests of many rows, where they
+ * are enough work for the tensor-core kernel, also v_j rounded to bf16 (once, from s*c + m).  Which kernel takes a
+ * request, and how its sum is split, follows from all lengths of the call: beside other requests the last bits of
+ * its output may differ.  Nothing overflows while |q| is at most 2^80, |v| at most 2^56 and the sum of |q| |k|
+ * over the channels, times the scale, at most 2^120.
  *  q      [n_tokens][q_heads][d] with q_ld elements between tokens; request r's rows are q_start[r] ..
  *         q_start[r] + q_len[r] - 1.  Rows of no request are neither read nor written.
  *  q_start, q_len, kv_len [n_requests] (n_requests <= 8192), on the device; max_q_len: no q_len is larger.
@@ -418,8 +423,8 @@ PBSA_API pbsa_status pbsa_expand_q4(const pbsa_req_geom* g, const void* pool, in
  *  lse nullable out [q_heads][n_tokens].
  *  flags  0 or PBSA_CAUSAL.
  * A request whose numbers lie out of range (q_len > max_q_len, rows outside q, kv_len > 64 table_ld) is
- * left out and recorded; a slot outside the pool is recorded and its tokens are left out of the sums.
- * Deterministic for a given device. */
+ * left out and recorded (with n_tokens or max_q_len 0 no number is looked at); a slot outside the pool is recorded and its tokens are left out of the sums.
+ * The same call on the same device gives the same bits. */
 #define PBSA_CAUSAL 1
 PBSA_API pbsa_status pbsa_attend_q4(const pbsa_req_geom* g, const void* q, long long q_ld, int n_tokens,
                            const int* q_start, const int* q_len, const int* kv_len, int n_requests, int max_q_len,

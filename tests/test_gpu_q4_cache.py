@@ -152,3 +152,18 @@ def test_values_past_the_range_reach_only_the_rows_that_see_them(lens, heavy):
     f.check(o, lse, True)
     n = lens[0][0]
     assert torch.isnan(o[n - 1, :2]).all() and torch.isfinite(o[:n - 1]).all() and torch.isfinite(o[n:]).all()
+
+
+def test_expand_rounds_to_fp32_and_from_there_to_bf16():
+    """Code 3 of a token from -2^-30 to 15.0625 (s = 129/128) stands for 3.0234375 - 2^-30, next to the middle of two bf16
+    numbers: fp32 rounds it to the middle, which goes to the even one above."""
+    x = torch.full((1, 1, 64), 15.0625, dtype=torch.bfloat16)
+    x[0, 0, 0], x[0, 0, 1] = -2.0 ** -30, 3.015625
+    g = P.make_req_geom(1, 1, 64, 0.125, "bf16")
+    pool = torch.zeros((1, 1, P.pbsa_q4_block_bytes(g)), dtype=torch.uint8, device=DEV)
+    P.pbsa_append_q4(g, x.to(DEV), x.to(DEV), torch.zeros(1, dtype=torch.int32, device=DEV), pool, 1)
+    for t in _expand(g, pool, 1, 1, 64, torch.bfloat16):
+        assert float(t[0, 0, 1]) == 3.03125
+    f = P.make_req_geom(1, 1, 64, 0.125, "f32")
+    for t in _expand(f, pool, 1, 1, 64, torch.float32):
+        assert float(t[0, 0, 1]) == 3.0234375
