@@ -51,26 +51,9 @@ struct AttendQ4Params {
 };
 
 // a / b of non-negative numbers; 64-bit divisions are an order slower and rarely needed
-__device__ __forceinline__ long long quotient(long long a, long long b) {
+__host__ __device__ __forceinline__ long long quotient(long long a, long long b) {
   if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
   return a / b;
-}
-
-// sum over i in [0, n) of floor((a i + b) / m), for a, b >= 0, m > 0
-__device__ __forceinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
-  long long sum = 0;
-  while (true) {
-    sum += (n - 1) * n / 2 * (a / m) + n * (b / m);
-    a %= m;
-    b %= m;
-    const long long y = a * n + b;
-    if (y < m) return sum;
-    n = y / m;
-    b = y % m;
-    const long long t = m;
-    m = a;
-    a = t;
-  }
 }
 
 // The work of one request: row tiles of each kv head, and what a tile is charged in blocks.  Without the
@@ -83,16 +66,24 @@ struct Q4Request {
   int base;          // blocks(past), or -1: every tile is charged `blocks`
   int num, den;      // tile_rows, 64 * group
 
-  __device__ long long charged_to(int n) const {   // the first n tiles
+  __host__ __device__ long long charged_to(int n) const {   // the first n tiles
     if (base < 0) return (long long)n * blocks;
-    if (n == 0) return 0;
     if ((uint32_t)den % (uint32_t)num == 0) {      // sum of ceil(k / per): whole groups of `per` tiles, and the rest
       const int per = (uint32_t)den / (uint32_t)num, whole = (uint32_t)n / (uint32_t)per, rest = n - whole * per;
       return (long long)n * base + ((long long)whole * (whole + 1) / 2 * per + (long long)rest * (whole + 1));
     }
-    return (long long)n * base + floor_sum(n, den, num, num + den - 1);
+    // Otherwise tile_rows = 64 t, and ceil(t k / group) is the number of whole j >= 0 with k > j group / t: up to k = r that
+    // makes sum over j of max(0, r - floor(j group / t)).  `group` tiles on, the charge is t more.
+    const int t = num / BT, group = den / BT, whole = (uint32_t)n / (uint32_t)group, rest = n - whole * group;
+    long long period = 0, last = (long long)t * whole * rest;
+    for (int j = 0; j < t; ++j) {
+      const int from = (uint32_t)(j * group) / (uint32_t)t;
+      period += group - from;
+      last += rest > from ? rest - from : 0;
+    }
+    return (long long)n * base + (long long)whole * (whole - 1) / 2 * t * group + whole * period + last;
   }
-  __device__ int charge(int mt) const {
+  __host__ __device__ int charge(int mt) const {
     return base < 0 ? blocks : base + (int)quotient((long long)num * (mt + 1) + den - 1, den);
   }
   __device__ long long head_steps() const { return charged_to(tiles); }
