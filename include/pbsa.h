@@ -413,8 +413,8 @@ PBSA_API pbsa_status pbsa_expand_q4(const pbsa_req_geom* g, const void* pool, in
  * pool holds.  A token without keys gives o = 0 and lse = -inf.
  * Sums are fp32.  With PBSA_BF16 the products take weights rounded to bf16, and requests of many rows, where they
  * are enough work for the tensor-core kernel, also v_j rounded to bf16 (once, from s*c + m).  Which kernel takes a
- * request, and how its sum is split, follows from all lengths of the call: beside other requests the last bits of
- * its output may differ.  Nothing overflows while |q| is at most 2^80, |v| at most 2^56 and the sum of |q| |k|
+ * request, and how its sum is split, follows from all lengths of the call; in the tensor-core kernel a row's rounding
+ * also depends on its neighbours' scores: beside other requests or rows the last bits of an output may differ.  Nothing overflows while |q| is at most 2^80, |v| at most 2^56 and the sum of |q| |k|
  * over the channels, times the scale, at most 2^120.
  *  q      [n_tokens][q_heads][d] with q_ld elements between tokens; request r's rows are q_start[r] ..
  *         q_start[r] + q_len[r] - 1.  Rows of no request are neither read nor written.
@@ -423,7 +423,8 @@ PBSA_API pbsa_status pbsa_expand_q4(const pbsa_req_geom* g, const void* pool, in
  *  lse nullable out [q_heads][n_tokens].
  *  flags  0 or PBSA_CAUSAL.
  * A request whose numbers lie out of range (q_len > max_q_len, rows outside q, kv_len > 64 table_ld) is
- * left out and recorded (with n_tokens or max_q_len 0 no number is looked at); a slot outside the pool is recorded and its tokens are left out of the sums.
+ * left out and recorded (with n_tokens or max_q_len 0 no number is looked at); a slot outside the pool is
+ * recorded and its tokens are left out of the sums.
  * The same call on the same device gives the same bits. */
 #define PBSA_CAUSAL 1
 PBSA_API pbsa_status pbsa_attend_q4(const pbsa_req_geom* g, const void* q, long long q_ld, int n_tokens,
