@@ -28,7 +28,7 @@
 // error is recorded, copies in flight are waited for, and the kernel winds down.
 //
 // Measured (D = 128, bf16; 6.5 TB/s is a plain copy's rate): 32 tokens of 32 heads (8 kv heads) over 16000 .. 60000
-// cached ones, 1.37 GB: 287-300 us, 4.6-4.8 TB/s; the loads alone take 229 us.  48 tokens over 300 .. 8192, 229 MB:
+// cached ones, 1.37 GB: 287-309 us, 4.4-4.8 TB/s; the loads alone take 229 us.  48 tokens over 300 .. 8192, 229 MB:
 // 60 us, 3.8 TB/s.  One token of 12 heads over 1536: 8.8 us, of which the join and the launches are 3.
 // What bounds it: 290 warp instructions for 16 tokens of a head, 112 of them shifts and masks (128 codes a lane); the
 // issue slots are 56% busy, the integer pipe 60%, HBM 65-70%.  Three CTAs an SM at 128 registers: two (with four

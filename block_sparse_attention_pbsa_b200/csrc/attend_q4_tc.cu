@@ -33,9 +33,10 @@
 // Waits are bounded; on expiry the error is recorded and every role runs through its pieces without
 // waiting, drains its copies and MMAs, frees TMEM and returns.
 //
-// Measured (D = 128): 4608 tokens of 12 heads over 13824, without the causal rule: 653-659 us, 595 TFLOP/s (0.35 of
-// the measured 1685); three prompts of 700 .. 2048 tokens of 32 heads (8 kv heads) over 1000 .. 14000: 944-952 us, 565
-// TFLOP/s.  A step of 256 rows and 128 keys lasts about 5900 cycles; its MMAs take 2800 of the tensor pipe's, its
+// Measured (D = 128): 4608 tokens of 12 heads over 13824, without the causal rule: 650-681 us, 575-600 TFLOP/s (0.34-0.36 of
+// the measured 1685); three prompts of 700 .. 2048 tokens of 32 heads (8 kv heads) over 1000 .. 14000: 941-952 us, 565
+// TFLOP/s.  The same 4608 tokens over whole blocks that pbsa_expand_q4 has written out take pbsa_attend 305 us, 321-327
+// with the expansion (K rounded to bf16 there): a key is unpacked once a call and not once for each of 18 row tiles.  A step of 256 rows and 128 keys lasts about 5900 cycles; its MMAs take 2800 of the tensor pipe's, its
 // exponentials 2048 of either unit's.  What bounds it is the chain of a half: a pass over 128 scores a thread (about
 // 2900 cycles, the unpacking and the other half in the same issue slots), then 2300 until P V and the next Q K^T have
 // given the next S.  TMEM holds S and O of two halves and no third.  Earlier forms, when the chunk took 707 us and the
@@ -51,8 +52,8 @@ namespace {
 
 constexpr int TQ_THREADS = 640;      // warpgroups: control, unpack x 2, softmax x 2
 constexpr int TQ_ROWS = 256;         // two halves of 128
-// Blocks that are worth a CTA: with 4, 8, 16 and 32 one prompt of 300 tokens over 3000 took 49, 58, 70 and 90 us, 64
-// tokens over 30000 86, 77, 74 and 94 us.
+// Blocks that are worth a CTA: with 4, 8, 16 and 32 64 tokens of 8 heads over 2 and 30000 tokens take 58, 54, 61 and 84 us, 512
+// tokens of 12 heads over 2500 53, 53, 63 and 91, two requests of 256 tokens of 8 heads over 8000 64, 64, 63 and 86.
 constexpr int TQ_MIN_STEPS = 8;
 // Blocks that a tile's start and end and its second passes over masked steps cost: charged 0, 8, 12, 16 and 24, the three
 // prompts take 1063, 1003, 984, 984 and 1009 us, the chunk of 4608 tokens 672, 661, 664, 669 and 677.

@@ -13,7 +13,7 @@
 // heads, which take 10.1 us (3.6 TB/s).  It is bound by issue: about 130 warp instructions a token and head, most
 // of them per thread (range, scale, addresses), which is why a thread holds as many channels as one
 // group of V's layout.  With 8 channels a thread they were 216, and 15.2 us.
-// expand moves the same bytes the other way in 6.1 us (5.9 TB/s), bound by HBM.
+// expand moves the same bytes the other way in 6.1-6.3 us (5.7-5.9 TB/s), bound by HBM.
 #include "internal.h"
 #include "q4.cuh"
 
