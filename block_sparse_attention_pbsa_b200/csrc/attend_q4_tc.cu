@@ -408,8 +408,10 @@ __global__ void __launch_bounds__(TQ_THREADS, 1) attend_q4_tc_kernel(const Atten
           {   // key t: its scale, and what the sum of the row is multiplied by (see the top of the file)
             const float m = hi_bf16(ksm);
             float s = lo_bf16(ksm);
-            // a scale that is nothing beside the minimum (0: all channels are m): the minimum alone, scaled by itself
-            if (s <= fabsf(m) * 0x1p-60f) s = m == 0.f ? 1.f : fabsf(m);
+            // A scale of 0 (all channels are m, all codes 0): the product is (128 + r) sum(q) = m / s sum(q) in any s.  One far
+            // below the minimum keeps what the two large terms leave of their roundings, 2^-20 of 128 s |q|, below the
+            // score's own; with s = |m| (1 for zeros) it was up to 2^-13 of m |q|.
+            if (s == 0.f) s = fmaxf(fabsf(m) * 0x1p-12f, 0x1p-126f);
             const float r = __fdiv_rn(m, s) - 128.f;
             const float r2 = bf16_rest(r), r3 = bf16_rest(r2);
             const uint32_t r11 = pack_bf16(r, r);

@@ -131,6 +131,21 @@ def test_a_query_that_is_not_finite_stays_in_its_row(lens, heavy, value):
     assert P.pbsa_get_device_error(f.ws) == 0
 
 
+@pytest.mark.parametrize("heavy", [False, True])
+@pytest.mark.parametrize("value", [0.0, 0.5, -3.0, 1e-39])
+def test_keys_with_equal_channels(heavy, value):
+    """Keys whose channels are all one number (zeros, above all) have a scale of 0 and their score from the minimum alone, beside
+    small keys and queries with one large channel."""
+    def edit(f):
+        n, p = f.lens[0]
+        f.k[:n + p] *= 1e-3
+        f.k[:n + p][torch.arange(n + p) % 3 > 0] = value
+
+    f = Filled([(90, 50), (1, 60)], 4, 2, 128, "bf16", seed=38, edit=edit, heavy=heavy)
+    f.q[:, :, 0] *= 1e5
+    f.check(*f.attend(True), True)
+
+
 FIRST = """
 import sys, torch
 sys.path.insert(0, sys.argv[1])
