@@ -169,8 +169,12 @@ __global__ void __launch_bounds__(RT_THREADS) request_tables_kernel(const Tables
     return v < cnt ? p.free_slot[v] : given_back((int)(v - cnt));
   };
   const int t0 = rank * RT_THREADS + tid, stride = nctas * RT_THREADS;
-  // blocks given back that stay free
-  for (int v = cnt + t0; v < left; v += stride) p.free_slot[v] = given_back(v - cnt);
+  // blocks given back that stay free (those that are taken again are looked at with their rows)
+  for (int v = cnt + t0; v < left; v += stride) {
+    const int slot = given_back(v - cnt);
+    if (slot < 0 || slot >= p.pool_slots) record_error(p.ws, PBSA_ERR_DEVICE_INDEX, slot, K_REQ_TABLES);
+    p.free_slot[v] = slot;
+  }
   // new table entries
   for (int i = t0; i < taken; i += stride) {
     const int r = first_above(s_upto, p.R, i);

@@ -384,7 +384,8 @@ PBSA_API size_t pbsa_attend_q4_workspace_bytes(const pbsa_req_geom* g);
  *  kv_len may be seq_len, and free_cnt_out may be free_cnt (a state kept in place); otherwise outputs
  *  and inputs are distinct.  With both kept apart, the same call can be repeated.
  * A length outside [0, 64 table_ld], a free count outside [0, pool_slots] or a slot outside the pool is
- * recorded (ws, nullable) and the request or row is not served; a bad length counts as 0. */
+ * recorded (ws, nullable) and the request or row is not served; a bad length counts as 0, and a bad slot that is
+ * given back goes to the stack as it is. */
 PBSA_API pbsa_status pbsa_request_tables(const int* step_len, const int* seq_len, int n_requests, int* block_table,
                                 int table_ld, int* free_slot, const int* free_cnt, int pool_slots, int n_tokens,
                                 int* q_start, int* q_len, int* kv_len, int* free_cnt_out, int* slot_map,

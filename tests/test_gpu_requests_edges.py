@@ -191,3 +191,17 @@ def test_the_first_calls_of_a_process_may_be_captured(tmp_path, work):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, str(code), root, work], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_a_bad_slot_given_back_is_recorded(in_place):
+    """An ended request's table lists a slot outside the pool: it goes back on the stack as it is, recorded."""
+    i = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    for bad in (9, -1, 2 ** 31 - 1):
+        table, stack, seq, cnt = i(3, bad, 5, 6).view(2, 2), i(0, 1, 2, 4, 7, 7, 7, 7, 7), i(100, 70), i(4)
+        out, ws = [torch.zeros(n, dtype=torch.int32, device=DEV) for n in (3, 2, 2, 1, 3)], torch.zeros(256, dtype=torch.uint8, device=DEV)
+        kv, left = (seq, cnt) if in_place else (out[2], out[3])
+        P.pbsa_request_tables(i(-1, 3), seq, table, stack, cnt, out[0], out[1], kv, left, out[4], ws=ws)
+        assert stack.tolist() == [0, 1, 2, 4, 3, bad, 7, 7, 7] and left.tolist() == [6] and kv.tolist() == [0, 73]
+        assert out[4].tolist() == [6 * 64 + 6 + j for j in range(3)]
+        assert P.pbsa_get_device_error(ws) == 5
