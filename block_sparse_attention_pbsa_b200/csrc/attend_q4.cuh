@@ -375,7 +375,8 @@ __device__ __forceinline__ void q4_join_row(const AttendQ4Params& p, const Q4Des
 // Joins the pieces of both kernels.  The first `few` CTAs take a tile of the few-rows kernel each.  The others list the
 // tensor-core kernel's tiles (each for itself) and share their rows, 8 at a time: there may be one tile of a hundred
 // pieces or a hundred tiles of two.  (With 8 CTAs for each tile, 64 tokens of 8 heads over 2 and 30000 tokens take 85 us,
-// like this 54, two requests of 256 tokens over 8000 71 and 64; such a list of the few-rows kernel's tiles would cost single tokens 0.8 us.)
+// like this 54, two requests of 256 tokens over 8000 71 and 64; such a list of the few-rows kernel's tiles would cost
+// single tokens 0.8 us.)
 struct Q4JoinParams {
   AttendQ4Params p;          // descriptors and pieces are the few-rows kernel's
   const Q4Desc* tc_desc;     // ... and these the tensor-core kernel's

@@ -11,8 +11,8 @@
 //  * Each step covers two blocks (128 keys).  One thread each brings K's and V's bytes with bulk copies;
 //    two warpgroups, alternate steps, unpack them into shared-memory operand tiles (128-byte swizzle): K as
 //    the codes themselves (plus 128, exact in bf16), V as bf16 values s*c + m, rounded once (pbsa_expand_q4 rounds to fp32
-//    first, so a value next to the middle of two bf16 numbers may differ by a step).  The scores carry no rounding of K (to bf16 it would put 2^-8 |q . k| / sqrt(d) of
-//    noise into each):
+//    first, so a value next to the middle of two bf16 numbers may differ by a step).  The scores carry no rounding of K
+//    (to bf16 it would put 2^-8 |q . k| / sqrt(d) of noise into each):
 //      q . k = s (q . (c + 128) + (m / s - 128) sum(q)).
 //    The bracket is one product: (m / s - 128) and sum(q) as three bf16 terms each make a further slice of 16
 //    columns of K and Q.  The scale, times the softmax scale, is applied to the scores in fp32, together with the
@@ -36,8 +36,9 @@
 // Measured (D = 128): 4608 tokens of 12 heads over 13824, without the causal rule: 650-681 us, 575-600 TFLOP/s (0.34-0.36 of
 // the measured 1685); three prompts of 700 .. 2048 tokens of 32 heads (8 kv heads) over 1000 .. 14000: 941-952 us, 565
 // TFLOP/s.  The same 4608 tokens over whole blocks that pbsa_expand_q4 has written out take pbsa_attend 305 us, 321-327
-// with the expansion (K rounded to bf16 there): a key is unpacked once a call and not once for each of 18 row tiles.  A step of 256 rows and 128 keys lasts about 5900 cycles; its MMAs take 2800 of the tensor pipe's, its
-// exponentials 2048 of either unit's.  What bounds it is the chain of a half: a pass over 128 scores a thread (about
+// with the expansion (K rounded to bf16 there): a key is unpacked once a call and not once for each of 18 row tiles.
+// A step of 256 rows and 128 keys lasts about 5900 cycles; its MMAs take 2800 of the tensor pipe's, its exponentials
+// 2048 of either unit's.  What bounds it is the chain of a half: a pass over 128 scores a thread (about
 // 2900 cycles, the unpacking and the other half in the same issue slots), then 2300 until P V and the next Q K^T have
 // given the next S.  TMEM holds S and O of two halves and no third.  Earlier forms, when the chunk took 707 us and the
 // prompts 1168: two threads a row 819 and 1219 (registers), the maximum found before the exponentials 799 and 1205;

@@ -415,8 +415,9 @@ PBSA_API pbsa_status pbsa_expand_q4(const pbsa_req_geom* g, const void* pool, in
  * Sums are fp32.  With PBSA_BF16 the products take weights rounded to bf16, and requests of many rows, where they
  * are enough work for the tensor-core kernel, also v_j rounded to bf16 (once, from s*c + m).  Which kernel takes a
  * request, and how its sum is split, follows from all lengths of the call; in the tensor-core kernel a row's rounding
- * also depends on its neighbours' scores: beside other requests or rows the last bits of an output may differ.  Nothing overflows while |q| is at most 2^80, |v| at most 2^56 and the sum of |q| |k|
- * over the channels, times the scale, at most 2^120.
+ * also depends on its neighbours' scores: beside other requests or rows the last bits of an output may differ.
+ * Nothing overflows while |q| is at most 2^80, |v| at most 2^56 and the sum of |q| |k| over the channels, times the
+ * scale, at most 2^120.
  *  q      [n_tokens][q_heads][d] with q_ld elements between tokens; request r's rows are q_start[r] ..
  *         q_start[r] + q_len[r] - 1.  Rows of no request are neither read nor written.
  *  q_start, q_len, kv_len [n_requests] (n_requests <= 8192), on the device; max_q_len: no q_len is larger.
