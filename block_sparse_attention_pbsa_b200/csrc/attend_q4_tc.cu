@@ -33,8 +33,8 @@
 // Waits are bounded; on expiry the error is recorded and every role runs through its pieces without
 // waiting, drains its copies and MMAs, frees TMEM and returns.
 //
-// Measured (D = 128): 4608 tokens of 12 heads over 13824, without the causal rule: 650-681 us, 575-600 TFLOP/s (0.34-0.36 of
-// the measured 1685); three prompts of 700 .. 2048 tokens of 32 heads (8 kv heads) over 1000 .. 14000: 941-952 us, 565
+// Measured (D = 128): 4608 tokens of 12 heads over 13824, without the causal rule: 647-681 us, 575-605 TFLOP/s (0.34-0.36 of
+// the measured 1685); three prompts of 700 .. 2048 tokens of 32 heads (8 kv heads) over 1000 .. 14000: 937-952 us, 565-570
 // TFLOP/s.  The same 4608 tokens over whole blocks that pbsa_expand_q4 has written out take pbsa_attend 305 us, 321-327
 // with the expansion (K rounded to bf16 there): a key is unpacked once a call and not once for each of 18 row tiles.
 // A step of 256 rows and 128 keys lasts about 5900 cycles; its MMAs take 2800 of the tensor pipe's, its exponentials
